@@ -113,6 +113,46 @@ PA_API int pa_reshape_and_cache(const void* key, const void* value, pa_dtype src
                                 int num_blocks, int* err_flag, pa_stream_t stream);
 
 /*
+ * pa_rope_and_cache -- rotary positions with several axes on new tokens' query and
+ * key rows, and the cache write of the turned keys and the values, in one launch:
+ * what a layer does between its projections and pa_decode_* / pa_prefill*.
+ *
+ * Pair i (0 <= i < rotary_dim / 2) of a row turns by
+ *   angle = positions[pair_axis[i]][token] * inv_freq[i]   (64 bits)
+ *   (a, b) -> (a cos - b sin, a sin + b cos)
+ * with (a, b) = elements (i, i + rotary_dim / 2) (interleaved = 0) or (2i, 2i + 1)
+ * (interleaved = 1).  Elements from rotary_dim on pass unchanged.  One axis is the
+ * usual text form; time, height and width are three.
+ *
+ *   out            [num_tokens, num_heads, head_dim], dtype src_dtype, dense: the turned
+ *                  query rows, rounded once.  May be q itself if q is dense; no other
+ *                  overlap.
+ *   q, key, value  src_dtype (PA_F32, PA_F16, PA_BF16): token t's rows, dense
+ *                  [num_heads or num_kv_heads, head_dim], start at element t * stride
+ *                  (slices of one fused projection need no copy).  Strides are multiples
+ *                  of 16 bytes, at least a token's own rows.
+ *   positions      int64 [num_axes, num_tokens]; any value (|position| up to 2^31
+ *                  keeps the angle exact to 1e-6).
+ *   inv_freq       double [rotary_dim / 2].
+ *   pair_axis      int32 [rotary_dim / 2]; a pair whose axis is outside
+ *                  [0, num_axes) is not turned.
+ *   rotary_dim     a multiple of 16, 16 <= rotary_dim <= head_dim.
+ *   k_cache .. err_flag   as pa_reshape_and_cache: the slots, the dtypes and the
+ *                  quantisation, which takes the turned key in fp32.  A negative slot
+ *                  writes no cache row (its query row is still turned).  Caches must be
+ *                  16-byte aligned.
+ *   num_tokens may be 0 (nothing is launched).
+ */
+PA_API int pa_rope_and_cache(void* out, const void* q, const void* key, const void* value,
+                             pa_dtype src_dtype, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const int64_t* positions, int num_axes,
+                             const double* inv_freq, const int32_t* pair_axis, int rotary_dim,
+                             int interleaved, void* k_cache, void* v_cache, pa_dtype cache_dtype,
+                             float* k_scale, float* v_scale, const int64_t* slot_mapping,
+                             int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                             int block_size, int num_blocks, int* err_flag, pa_stream_t stream);
+
+/*
  * pa_prefill -- multi-token query over the paged cache: each sequence's last
  * q_len tokens (already written to the cache, e.g. by pa_reshape_and_cache)
  * attend causally to every cached token up to and including themselves.  This

@@ -238,6 +238,69 @@ PA_API int pa_reshape_and_cache(const void* key, const void* value, pa_dtype src
   return cuda_status(e);
 }
 
+PA_API int pa_rope_and_cache(void* out, const void* q, const void* key, const void* value,
+                             pa_dtype src_dtype, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const int64_t* positions, int num_axes,
+                             const double* inv_freq, const int32_t* pair_axis, int rotary_dim,
+                             int interleaved, void* k_cache, void* v_cache, pa_dtype cache_dtype,
+                             float* k_scale, float* v_scale, const int64_t* slot_mapping,
+                             int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                             int block_size, int num_blocks, int* err_flag, pa_stream_t stream) {
+  if (num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 || num_axes <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (!block_size_ok(block_size) || interleaved < 0 || interleaved > 1) return PA_ERR_INVALID_ARG;
+  if (!is_float(src_dtype) || cache_dtype < PA_F32 || cache_dtype > PA_FP8E4M3)
+    return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (!is_quant(cache_dtype) && cache_dtype != src_dtype) return PA_ERR_UNSUPPORTED;
+  if (num_heads > (1 << 20) || num_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!out || !q || !key || !value || !positions || !inv_freq || !pair_axis || !k_cache ||
+      !v_cache || !slot_mapping)
+    return PA_ERR_INVALID_ARG;
+  if (is_quant(cache_dtype) && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  const int64_t ve = 16 / elem_bytes(src_dtype);
+  const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (q_stride % ve != 0 || k_stride % ve != 0 || v_stride % ve != 0 || q_stride < q_row ||
+      k_stride < kv_row || v_stride < kv_row)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8) ||
+      !aligned(positions, 8) || !aligned(inv_freq, 8) || !aligned(pair_axis, 4))
+    return PA_ERR_INVALID_ARG;
+  if (is_quant(cache_dtype) && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))
+    return PA_ERR_INVALID_ARG;
+  pa::RopeArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k = key;
+  a.v = value;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.pair_axis = pair_axis;
+  a.slots = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.err_flag = err_flag;
+  a.num_tokens = num_tokens;
+  a.num_axes = num_axes;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  return cuda_status(pa::launch_rope(a, src_dtype, cache_dtype, head_dim,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
 namespace {
 
 // pa_decode_v1, with the fused write of each sequence's new token when new_k is

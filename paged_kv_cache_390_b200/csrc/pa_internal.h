@@ -98,6 +98,29 @@ cudaError_t launch_reshape_and_cache(const void* key, const void* value, int src
                                      int num_kv_heads, int head_dim, int block_size,
                                      int num_blocks, int* err_flag, cudaStream_t stream);
 
+// Rotary positions and the cache write (pa_rope_and_cache).
+struct RopeArgs {
+  void* out;                  // [T, H, D] in the source dtype
+  const void* q;              // rows of H x D, K and V rows of H_kv x D; strides in elements
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const int64_t* positions;   // [num_axes, T]
+  const double* inv_freq;     // [rotary_dim / 2]
+  const int32_t* pair_axis;   // [rotary_dim / 2]
+  const int64_t* slots;       // [T]
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int* err_flag;
+  int num_tokens, num_axes, rotary_dim, interleaved;
+  int num_heads, num_kv_heads, block_size, num_blocks;
+};
+
+cudaError_t launch_rope(const RopeArgs& a, int src_dtype, int cache_dtype, int head_dim,
+                        cudaStream_t s);
+
 // Persistent single-launch decode (pa_decode_fused): every warp streams an
 // equal contiguous range of the batch's 16-token tiles; a (sequence, kv head)
 // split between warps is merged by the warp that finishes it last.

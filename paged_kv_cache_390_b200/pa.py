@@ -7,6 +7,7 @@ is no fallback: if the library is missing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -45,6 +46,7 @@ def lib() -> ctypes.CDLL:
                 " (there is no fallback path)")
         L = ctypes.CDLL(LIB_PATH)
         P, I, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        LL = ctypes.c_int64
         sigs = {
             "pa_reshape_and_cache": (I, [P, P, I, P, P, I, P, P, P, I, I, I, I, I, P, P]),
             "pa_decode_v1": (I, [P, P, I, P, P, I, P, P, P, I, P, I, I, I, I, I, I, F, P, P]),
@@ -76,6 +78,8 @@ def lib() -> ctypes.CDLL:
             "pa_decode_cascade_workspace_bytes": (S, [I, I, I]),
             "pa_set_cascade_config": (I, [I, I]),
             "pa_prefill": (I, [P, P, I, P, I, I, P, P, I, P, I, P, I, I, I, I, I, I, F, P, P]),
+            "pa_rope_and_cache": (I, [P, P, P, P, I, LL, LL, LL, P, I, P, P, I, I, P, P, I, P, P,
+                                      P, I, I, I, I, I, I, P, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -112,6 +116,57 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _same_device(*tensors) -> torch.device:
+    """The CUDA device that all the tensors are on."""
+    dev = tensors[0].device
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to libpa must be CUDA tensors")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors of one call must be on one CUDA device")
+    return dev
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """Make `dev` current, and `stream` (if given) torch's stream there, so that what the
+    call allocates belongs to the stream that uses it; yields the stream's handle."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream().cuda_stream
+    elif stream is None:
+        with torch.cuda.device(dev):
+            yield torch.cuda.current_stream().cuda_stream
+    else:
+        if stream.device != dev:
+            raise ValueError("the stream and the tensors must be on one CUDA device")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _row_stride(t) -> int:
+    """Token stride of [T, heads, D] rows whose last two dimensions are dense."""
+    T, heads, D = t.shape
+    if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        raise ValueError("a token's rows must be dense")
+    return t.stride(0) if T > 1 else heads * D
+
+
+def _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype) -> int:
+    """Shapes and dtypes of the paged pool and its scales; the cache dtype's code."""
+    code = cache_code(k_cache, cache_dtype)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have the same shape and dtype")
+    if k_cache.element_size() != (4, 2, 2, 1, 1)[code]:
+        raise ValueError("the cache tensor's element size does not fit cache_dtype")
+    if code in (PA_INT8, PA_FP8E4M3):
+        num_blocks, block_size, num_kv_heads, _ = k_cache.shape
+        for t in (k_scale, v_scale):
+            if t is None or t.dtype != torch.float32 or t.shape != (num_blocks, num_kv_heads,
+                                                                    block_size):
+                raise ValueError("scales must be float32 [num_blocks, num_kv_heads, block_size]")
+    return code
+
+
 def cache_code(cache: torch.Tensor, cache_dtype: str | None = None) -> int:
     if cache_dtype is not None:
         return CACHE_CODES[cache_dtype]
@@ -135,6 +190,67 @@ def reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, *, cache_dtype
         key.shape[0], num_kv_heads, head_dim, block_size, num_blocks, _ptr(err_flag),
         _stream(stream))
     _check(rc, "pa_reshape_and_cache")
+
+
+def rope_inv_freq(rotary_dim, base=10000.0, device="cuda") -> torch.Tensor:
+    """inv_freq of pa_rope_and_cache: base ** (-2 i / rotary_dim), in 64 bits."""
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    return (float(base) ** (-i / rotary_dim)).to(device)
+
+
+def rope_pair_axis(sections, spread=False, device="cuda") -> torch.Tensor:
+    """pair_axis of pa_rope_and_cache for axes that own sections[a] pairs each: whole
+    runs in the axes' order, or (spread) the axes in turn until each has its share."""
+    if spread:
+        left, axis = [int(n) for n in sections], []
+        while any(left):
+            for a in range(len(left)):
+                if left[a]:
+                    left[a] -= 1
+                    axis.append(a)
+    else:
+        axis = [a for a, n in enumerate(sections) for _ in range(int(n))]
+    return torch.tensor(axis, dtype=torch.int32, device=device)
+
+
+def rope_and_cache(q, key, value, positions, inv_freq, pair_axis, k_cache, v_cache, slot_mapping,
+                   *, interleaved=False, out=None, cache_dtype=None, k_scale=None, v_scale=None,
+                   err_flag=None, stream=None) -> torch.Tensor:
+    """Turn the query and key rows of new tokens by their rotary positions (several axes:
+    positions int64 [axes, T], or [T] for one) and write the turned keys and the values
+    to the paged cache, in one launch; returns the turned queries.  q [T, H, D] and key,
+    value [T, H_kv, D] may be slices of a fused projection (rows dense, any token
+    stride); out=q turns dense queries in place."""
+    num_blocks, block_size, num_kv_heads, head_dim = k_cache.shape
+    num_tokens, num_heads, _ = q.shape
+    num_axes = positions.shape[0] if positions.dim() == 2 else 1
+    if (q.shape[2] != head_dim or key.shape != (num_tokens, num_kv_heads, head_dim)
+            or value.shape != key.shape or v_cache.shape != k_cache.shape
+            or positions.shape[-1] != num_tokens or slot_mapping.shape != (num_tokens,)
+            or pair_axis.shape != inv_freq.shape or inv_freq.dim() != 1):
+        raise ValueError("shapes of q, key, value, positions, slots, frequencies and caches differ")
+    if key.dtype != q.dtype or value.dtype != q.dtype:
+        raise ValueError("key and value must have q's dtype")
+    if (positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64
+            or inv_freq.dtype != torch.float64 or pair_axis.dtype != torch.int32):
+        raise ValueError("positions and slots are int64, inv_freq float64, pair_axis int32")
+    code = _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype)
+    dev = _same_device(q, key, value, positions, inv_freq, pair_axis, k_cache, v_cache,
+                       slot_mapping, k_scale, v_scale, err_flag, out)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((num_tokens, num_heads, head_dim), dtype=q.dtype, device=dev)
+        elif out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must have q's shape and dtype")
+        rc = lib().pa_rope_and_cache(
+            _ptr(out), q.data_ptr(), key.data_ptr(), value.data_ptr(), _FLOAT_CODES[q.dtype],
+            _row_stride(q), _row_stride(key), _row_stride(value), _ptr(positions), num_axes,
+            _ptr(inv_freq), _ptr(pair_axis), 2 * inv_freq.shape[0], int(bool(interleaved)),
+            _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
+            num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, _ptr(err_flag),
+            s)
+    _check(rc, "pa_rope_and_cache")
+    return out
 
 
 def copy_blocks(src_k, src_v, dst_k, dst_v, block_mapping, *, cache_dtype=None,
