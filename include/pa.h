@@ -280,6 +280,48 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
                           int head_dim, int block_size, int* err_flag, pa_stream_t stream);
 
 /*
+ * pa_evict -- cut cached sequences down to num_keep tokens by accumulated attention
+ * weight: per (sequence, kv head) the num_recent newest tokens stay and, of the others,
+ * the num_keep - num_recent with the highest scores (equal scores: the earlier token),
+ * in their order.  A sequence of at most num_keep tokens keeps all of them.  Each
+ * kv head keeps its own tokens; a sequence's heads all keep new_lens[s] =
+ * min(seq_lens[s], num_keep) of them, so the result is again a paged cache of shorter
+ * sequences.  The kept rows (and scales) are copied bit for bit to token places
+ * 0, 1, ... of the sequence's new block table; the source blocks are only read, so
+ * blocks shared with other sequences are safe.  pa_bm_evict hands out the new tables.
+ * Scores come from pa_decode_masked.  Keys keep the positions they were turned by;
+ * a bias by distance or a window counts places of the shorter cache from then on.
+ *
+ *   k_cache .. v_scale   the pool, read and written; as pa_reshape_and_cache.
+ *   block_tables   int32 [num_seqs, max_blocks_per_seq], seq_lens int32 [num_seqs]: the
+ *                  sequences as they are.
+ *   new_block_tables  int32 [num_seqs, max_new_blocks]: where they go.  A new block
+ *                  appears once and is not a source block of the call.
+ *   scores         fp32 [num_seqs, num_kv_heads, score_stride], one per cached token;
+ *                  NaN counts as lowest.
+ *   num_keep >= 1, 0 <= num_recent <= num_keep.
+ *   kept           int32 [num_seqs, num_kv_heads, kept_stride]: the kept tokens' old
+ *                  places, then -1.
+ *   new_scores     fp32 [num_seqs, num_kv_heads, new_score_stride] or NULL: the kept
+ *                  tokens' scores; places past new_lens[s] are left as they are.
+ *   new_lens       int32 [num_seqs]; neither new_lens nor new_scores may be the input
+ *                  they replace.
+ * Always checked: a sequence whose length is negative, past its table or past
+ * score_stride, or whose kept tokens do not fit new_block_tables, kept or new_scores,
+ * is skipped (new_lens 0, kept -1) and sets PA_DEVERR_SEQ_LEN; a row whose source or new
+ * block id is outside the pool is not copied and sets PA_DEVERR_BLOCK_ID (both also in
+ * the library's device error word).  Head sizes and block sizes as pa_decode_v1, any
+ * cache dtype, caches 16-byte aligned.  Deterministic.
+ */
+PA_API int pa_evict(void* k_cache, void* v_cache, pa_dtype cache_dtype, float* k_scale,
+                    float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                    const int32_t* seq_lens, const int32_t* new_block_tables, int max_new_blocks,
+                    const float* scores, int score_stride, int num_keep, int num_recent, int* kept,
+                    int kept_stride, float* new_scores, int new_score_stride, int* new_lens,
+                    int num_seqs, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                    int* err_flag, pa_stream_t stream);
+
+/*
  * pa_decode_v1 -- single-pass paged decode attention ([深度解析] §4.1
  * paged_attention_v1; kernel arguments as in [vllm-musa] §五):
  *   out[s, h, :] = sum_t softmax_t(scale * q[s,h,:] . K_t) V_t

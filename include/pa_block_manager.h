@@ -99,6 +99,17 @@ PA_API int pa_bm_swap_out(pa_block_manager* m, const int64_t* seq_ids, int num_s
 PA_API int pa_bm_swap_in(pa_block_manager* m, const int64_t* seq_ids, int num_seqs,
                          int64_t* mapping, int capacity, int* num_pairs);
 
+/* New blocks for sequences cut to num_keep tokens by pa_evict: each resident sequence of
+ * seq_ids[num_seqs] (distinct) gets ceil(min(tokens, num_keep) / block_size) fresh
+ * blocks, written to new_tables int32 [num_seqs][max_blocks] (padding -1), and lets go of
+ * its old ones.  Take the old tables with pa_bm_build_batch before this call, and enqueue
+ * pa_evict before anything that writes blocks handed out later.  All fresh blocks are
+ * taken before any old one is released, so no new block is a source of the same call.
+ * Each kv head of such a sequence keeps its own tokens: from here on its blocks are not
+ * offered to the prefix cache. */
+PA_API int pa_bm_evict(pa_block_manager* m, const int64_t* seq_ids, int num_seqs, int num_keep,
+                       int32_t* new_tables, int max_blocks);
+
 /* A sequence's block ids (table[capacity]), block count and token count.  The
  * counts are written even when capacity is too small (then PA_ERR_INVALID_ARG),
  * so a call with capacity 0 asks for the size. */

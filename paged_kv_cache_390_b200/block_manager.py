@@ -25,6 +25,7 @@ _SIGS = {
     "pa_bm_free_sequence": (_I, [_P, _L]),
     "pa_bm_swap_out": (_I, [_P, _P, _I, _P, _I, _P]),
     "pa_bm_swap_in": (_I, [_P, _P, _I, _P, _I, _P]),
+    "pa_bm_evict": (_I, [_P, _P, _I, _I, _P, _I]),
     "pa_bm_block_table": (_I, [_P, _L, _P, _I, _P, _P]),
     "pa_bm_build_batch": (_I, [_P, _P, _I, _P, _I, _P]),
 }
@@ -136,6 +137,16 @@ class BlockManager:
     def swap_in(self, seq_ids):
         """Returns the (cpu block, gpu block) pairs to copy."""
         return self._swap(_lib().pa_bm_swap_in, seq_ids)
+
+    def evict(self, seq_ids, num_keep: int):
+        """New block tables int32 [n, max_blocks] (padded with -1) for sequences cut to
+        num_keep tokens by ``pa.evict``; take their old ones (``build_batch``) first."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        width = -(-num_keep // self.block_size) if num_keep > 0 else 1
+        tables = np.empty((len(ids), width), dtype=np.int32)
+        rc = _lib().pa_bm_evict(self._h, _arr(ids), len(ids), num_keep, _arr(tables), width)
+        pa._check(rc, "pa_bm_evict")
+        return tables
 
     def block_table(self, seq_id: int):
         """Returns (block ids int32 [num_blocks], num_tokens)."""

@@ -230,7 +230,6 @@ PA_API int pa_reshape_and_cache(const void* key, const void* value, pa_dtype src
     return PA_ERR_INVALID_ARG;
   if (is_quant(cache_dtype) && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))
     return PA_ERR_INVALID_ARG;
-  (void)elem_bytes;
   cudaError_t e = pa::launch_reshape_and_cache(
       key, value, src_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, slot_mapping,
       num_tokens, num_kv_heads, head_dim, block_size, num_blocks, err_flag,
@@ -622,6 +621,67 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
   if (pa::copy_slices_per_pair(a.block_vecs, a.scale_vecs) > 65535) return PA_ERR_UNSUPPORTED;
   cudaError_t e = pa::launch_copy_blocks(a, num_pairs, reinterpret_cast<cudaStream_t>(stream));
   return cuda_status(e);
+}
+
+PA_API int pa_evict(void* k_cache, void* v_cache, pa_dtype cache_dtype, float* k_scale,
+                    float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                    const int32_t* seq_lens, const int32_t* new_block_tables, int max_new_blocks,
+                    const float* scores, int score_stride, int num_keep, int num_recent, int* kept,
+                    int kept_stride, float* new_scores, int new_score_stride, int* new_lens,
+                    int num_seqs, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                    int* err_flag, pa_stream_t stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 ||
+      max_new_blocks <= 0 || score_stride <= 0 || kept_stride <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_keep < 1 || num_recent < 0 || num_recent > num_keep) return PA_ERR_INVALID_ARG;
+  if (!block_size_ok(block_size)) return PA_ERR_INVALID_ARG;
+  if (cache_dtype < PA_F32 || cache_dtype > PA_FP8E4M3) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_blocks) * block_size > INT_MAX) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !seq_lens || !new_block_tables || !scores || !kept ||
+      !new_lens)
+    return PA_ERR_INVALID_ARG;
+  const bool quant = is_quant(cache_dtype);
+  if (quant && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if (new_scores && (new_score_stride <= 0 || new_scores == scores)) return PA_ERR_INVALID_ARG;
+  if (new_lens == seq_lens || new_block_tables == block_tables) return PA_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) ||
+      !aligned(seq_lens, 4) || !aligned(new_block_tables, 4) || !aligned(scores, 4) ||
+      !aligned(kept, 4) || !aligned(new_scores, 4) || !aligned(new_lens, 4) ||
+      (quant && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
+    return PA_ERR_INVALID_ARG;
+  pa::EvictArgs a{};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = quant ? k_scale : nullptr;
+  a.v_scale = quant ? v_scale : nullptr;
+  a.src_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.dst_tables = new_block_tables;
+  a.scores = scores;
+  a.kept = kept;
+  a.new_scores = new_scores;
+  a.new_lens = new_lens;
+  a.err_flag = err_flag;
+  a.max_src_blocks = max_blocks_per_seq;
+  a.max_dst_blocks = max_new_blocks;
+  a.score_stride = score_stride;
+  a.kept_stride = kept_stride;
+  a.new_score_stride = new_scores ? new_score_stride : 0;
+  a.num_keep = num_keep;
+  a.num_recent = num_recent;
+  const long long room = static_cast<long long>(max_new_blocks) * block_size;
+  long long most = std::min<long long>(num_keep, std::min<long long>(room, kept_stride));
+  if (new_scores) most = std::min<long long>(most, new_score_stride);
+  a.max_kept = static_cast<int>(most);
+  a.num_seqs = num_seqs;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.row_vecs = head_dim * elem_bytes(cache_dtype) / 16;
+  return cuda_status(pa::launch_evict(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 PA_API int pa_prefill(void* out, const void* q, pa_dtype q_dtype, const int32_t* query_start,

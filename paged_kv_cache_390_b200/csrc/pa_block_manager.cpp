@@ -72,6 +72,7 @@ struct Seq {
   std::vector<int32_t> tokens;
   bool on_gpu = true;
   uint64_t chain = 0;   // prefix caching: the key of the sequence's last full block
+  bool cut = false;     // evicted from: its blocks no longer hold its tokens one to one
 };
 
 struct Cached {
@@ -246,7 +247,7 @@ PA_API int pa_bm_append_token(pa_block_manager* m, int64_t seq_id, int32_t token
     }
   }
   s.tokens.push_back(token);
-  if (m->prefix && (n + 1) % bs == 0)          // block n / bs is full: key it off the chain
+  if (m->prefix && !s.cut && (n + 1) % bs == 0)   // block n / bs is full: key it off the chain
     s.chain = m->register_block(b, s.chain, s.tokens.data() + (n / bs) * bs);
   *slot = static_cast<int64_t>(b) * bs + n % bs;
   if (cow_src) *cow_src = src;
@@ -337,6 +338,48 @@ PA_API int pa_bm_swap_out(pa_block_manager* m, const int64_t* seq_ids, int num_s
 PA_API int pa_bm_swap_in(pa_block_manager* m, const int64_t* seq_ids, int num_seqs,
                          int64_t* mapping, int capacity, int* num_pairs) {
   return swap_group(m, seq_ids, num_seqs, mapping, capacity, num_pairs, false);
+}
+
+PA_API int pa_bm_evict(pa_block_manager* m, const int64_t* seq_ids, int num_seqs, int num_keep,
+                       int32_t* new_tables, int max_blocks) try {
+  if (!m || num_seqs < 0 || num_keep < 1 || max_blocks <= 0 ||
+      (num_seqs > 0 && (!seq_ids || !new_tables)))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  std::vector<int64_t> sorted(seq_ids, seq_ids + num_seqs);   // no sequence twice
+  std::sort(sorted.begin(), sorted.end());
+  if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end()) return PA_ERR_INVALID_ARG;
+  const long long bs = m->bs;
+  auto blocks_of = [&](const Seq& s) {
+    return static_cast<size_t>((std::min<long long>(s.tokens.size(), num_keep) + bs - 1) / bs);
+  };
+  size_t need = 0;
+  std::vector<std::vector<int32_t>> fresh(num_seqs);          // every allocation before any change
+  for (int i = 0; i < num_seqs; ++i) {
+    auto it = m->seqs.find(seq_ids[i]);
+    if (it == m->seqs.end() || !it->second.on_gpu) return PA_ERR_INVALID_ARG;
+    const size_t n = blocks_of(it->second);
+    if (n > static_cast<size_t>(max_blocks)) return PA_ERR_INVALID_ARG;
+    fresh[i].reserve(n);
+    need += n;
+  }
+  if (static_cast<size_t>(m->free_gpu()) < need) return PA_ERR_NO_SPACE;
+  for (int i = 0; i < num_seqs; ++i) {
+    Seq& s = m->seqs.find(seq_ids[i])->second;
+    const size_t n = blocks_of(s);
+    for (size_t b = 0; b < n; ++b) fresh[i].push_back(m->take_gpu());
+    s.blocks.swap(fresh[i]);                     // fresh[i] now holds the old ones
+    s.tokens.resize(std::min<size_t>(s.tokens.size(), num_keep));
+    s.cut = true;
+    int32_t* row = new_tables + static_cast<size_t>(i) * max_blocks;
+    std::copy(s.blocks.begin(), s.blocks.end(), row);
+    std::fill(row + n, row + max_blocks, -1);
+  }
+  for (const auto& old : fresh)
+    for (int32_t b : old) m->release_gpu(b);
+  return PA_OK;
+} catch (const std::bad_alloc&) {
+  return PA_ERR_NO_SPACE;
 }
 
 PA_API int pa_bm_block_table(const pa_block_manager* m, int64_t seq_id, int32_t* table,

@@ -121,6 +121,29 @@ struct RopeArgs {
 cudaError_t launch_rope(const RopeArgs& a, int src_dtype, int cache_dtype, int head_dim,
                         cudaStream_t s);
 
+// Eviction by accumulated attention weight (pa_evict).
+struct EvictArgs {
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;             // null: no scales
+  float* v_scale;
+  const int32_t* src_tables;  // [S, max_src_blocks]
+  const int32_t* seq_lens;
+  const int32_t* dst_tables;  // [S, max_dst_blocks]
+  const float* scores;        // [S, H_kv, score_stride]
+  int* kept;                  // [S, H_kv, kept_stride]
+  float* new_scores;          // [S, H_kv, new_score_stride] or null
+  int* new_lens;              // [S]
+  int* err_flag;
+  int max_src_blocks, max_dst_blocks, score_stride, kept_stride, new_score_stride;
+  int num_keep, num_recent;
+  int max_kept;               // places every output has room for, at most num_keep
+  int num_seqs, num_kv_heads, block_size, num_blocks;
+  int row_vecs;               // 16-byte vectors per (token, kv head) row
+};
+
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+
 // Persistent single-launch decode (pa_decode_fused): every warp streams an
 // equal contiguous range of the batch's 16-token tiles; a (sequence, kv head)
 // split between warps is merged by the warp that finishes it last.

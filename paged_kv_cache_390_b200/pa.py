@@ -80,6 +80,8 @@ def lib() -> ctypes.CDLL:
             "pa_prefill": (I, [P, P, I, P, I, I, P, P, I, P, I, P, I, I, I, I, I, I, F, P, P]),
             "pa_rope_and_cache": (I, [P, P, P, P, I, LL, LL, LL, P, I, P, P, I, I, P, P, I, P, P,
                                       P, I, I, I, I, I, I, P, P]),
+            "pa_evict": (I, [P, P, I, P, P, P, I, P, P, I, P, I, I, I, P, I, P, I, P, I, I, I, I, I,
+                             P, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)
@@ -149,6 +151,13 @@ def _row_stride(t) -> int:
     if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
         raise ValueError("a token's rows must be dense")
     return t.stride(0) if T > 1 else heads * D
+
+
+def _batch_checks(block_tables, seq_lens, num_seqs) -> None:
+    if (block_tables.dtype != torch.int32 or block_tables.dim() != 2
+            or block_tables.shape[0] != num_seqs or seq_lens.dtype != torch.int32
+            or seq_lens.shape != (num_seqs,)):
+        raise ValueError("block tables are int32 [num_seqs, width], lengths int32 [num_seqs]")
 
 
 def _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype) -> int:
@@ -275,6 +284,47 @@ def copy_blocks(src_k, src_v, dst_k, dst_v, block_mapping, *, cache_dtype=None,
         block_mapping.shape[0] if block_mapping.numel() else 0, num_kv_heads, head_dim,
         block_size, _ptr(err_flag), _stream(stream))
     _check(rc, "pa_copy_blocks")
+
+
+def evict(k_cache, v_cache, block_tables, seq_lens, new_block_tables, scores, num_keep, num_recent,
+          *, kept=None, new_scores=None, new_lens=None, cache_dtype=None, k_scale=None,
+          v_scale=None, err_flag=None, stream=None):
+    """Cut sequences down to num_keep tokens per kv head: the num_recent newest and the
+    highest-scored others, moved in their order to the blocks of new_block_tables (see
+    BlockManager.evict).  scores float32 [S, H_kv, width].  Returns (kept int32
+    [S, H_kv, num_keep], padded with -1; new_lens int32 [S]; new_scores)."""
+    num_blocks, block_size, num_kv_heads, head_dim = k_cache.shape
+    num_seqs = seq_lens.shape[0]
+    code = _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype)
+    _batch_checks(block_tables, seq_lens, num_seqs)
+    _batch_checks(new_block_tables, seq_lens, num_seqs)
+    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (num_seqs,
+                                                                                  num_kv_heads):
+        raise ValueError("scores must be float32 [num_seqs, num_kv_heads, width]")
+    dev = _same_device(k_cache, v_cache, block_tables, seq_lens, new_block_tables, scores, kept,
+                       new_scores, new_lens, k_scale, v_scale, err_flag)
+    with _on(dev, stream) as s:
+        if kept is None:
+            kept = torch.empty((num_seqs, num_kv_heads, num_keep), dtype=torch.int32, device=dev)
+        if new_scores is None:
+            new_scores = torch.zeros((num_seqs, num_kv_heads, num_keep), device=dev)
+        if new_lens is None:
+            new_lens = torch.empty(num_seqs, dtype=torch.int32, device=dev)
+        for t, dt in ((kept, torch.int32), (new_scores, torch.float32)):
+            if t.dtype != dt or t.dim() != 3 or t.shape[:2] != scores.shape[:2]:
+                raise ValueError("kept (int32) and new_scores (float32) are "
+                                 "[num_seqs, num_kv_heads, width]")
+        if new_lens.dtype != torch.int32 or new_lens.shape != (num_seqs,):
+            raise ValueError("new_lens must be int32 [num_seqs]")
+        rc = lib().pa_evict(
+            _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+            block_tables.shape[1], _ptr(seq_lens), _ptr(new_block_tables),
+            new_block_tables.shape[1], _ptr(scores), scores.shape[2], int(num_keep),
+            int(num_recent), _ptr(kept), kept.shape[2], _ptr(new_scores), new_scores.shape[2],
+            _ptr(new_lens), num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+            _ptr(err_flag), s)
+    _check(rc, "pa_evict")
+    return kept, new_lens, new_scores
 
 
 def decode_v1(q, k_cache, v_cache, block_tables, seq_lens, scale, *, out=None, cache_dtype=None,

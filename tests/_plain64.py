@@ -38,3 +38,21 @@ def rope_tol(x64, dt):
     mag = x64.abs().amax(-1, keepdim=True)
     tiny = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
     return half_step(dt) * x64.abs() * (1 + 2.0 ** -10) + 2 * mag * (4 + 3) * 2.0 ** -24 + tiny
+
+
+def evict(scores, lens, num_keep, num_recent):
+    """Kept token lists [S][H_kv], from the definition."""
+    out = []
+    for s, n in enumerate(lens):
+        per = []
+        for h in range(scores.shape[1]):
+            row = scores[s, h].tolist()
+            new = list(range(max(0, n - num_recent), n))
+            old = [i for i in range(max(0, n - num_recent))]
+            val = {i: (-math.inf if math.isnan(row[i]) else row[i]) for i in old}
+            # NaN below every number, then by score, then the earlier token
+            old.sort(key=lambda i: (math.isnan(row[i]), -val[i], i))
+            m = min(n, num_keep)
+            per.append(sorted(new + old[:m - len(new)]))
+        out.append(per)
+    return out
