@@ -280,6 +280,79 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
                           int head_dim, int block_size, int* err_flag, pa_stream_t stream);
 
 /*
+ * pa_decode_masked -- paged decode attention with changed scores.  Sequence s's new token
+ * is its last cached one, at position pos = seq_lens[s] - 1:
+ *   x_t = softcap * tanh(scale * q . K_t / softcap) - alibi_slopes[h] * |pos - t|
+ *   out[s, h, :] = sum_t softmax_t(x_t) V_t
+ * over the tokens it sees, max(kv_start[s], pos - window + 1) <= t <= pos.
+ *
+ *   softcap        > 0 and not below 2^-20 |scale|, or 0: x_t = scale * q . K_t - ...
+ *   alibi_slopes   fp32 [num_heads] (finite) or NULL: no bias.
+ *   kv_start       int32 [num_seqs] or NULL (0): the first token of the new token's
+ *                  document.  Values below 0 count as 0; at or past seq_lens[s] the
+ *                  sequence sees nothing.
+ *   window         tokens seen back from pos, itself included; 0: no limit.
+ *   scores_in, scores_out   fp32 [num_seqs, num_kv_heads, score_stride], both or only
+ *                  scores_out or neither; may be the same array.  For every cached token
+ *                  t < min(seq_lens[s], score_stride):
+ *                    scores_out[s, k, t] = scores_in[s, k, t] (or 0) +
+ *                       the sum over the query heads of kv head k of softmax_t(x_t)
+ *                  (0 added where the token is not seen).  Later places stay as they are.
+ *                  pa_evict takes these scores.
+ *   workspace      device memory, 256-byte aligned, at least
+ *                  pa_decode_masked_workspace_bytes(num_seqs, num_heads, num_kv_heads,
+ *                  head_dim, scores_out ? score_stride : 0) bytes, ZEROED BEFORE ITS FIRST
+ *                  USE and after a call that reported PA_DEVERR_TIMEOUT.  Calls that share
+ *                  a workspace (two captured graphs, two streams) must not overlap on the
+ *                  GPU.
+ *   Other arguments, types and err_flag as pa_decode_fused.  A sequence that sees nothing
+ *   gets zeros.  Whatever the rows of unseen tokens hold (infinities, NaN) does not reach
+ *   the output or the scores.  A sequence dropped for its length (err_flag) keeps its
+ *   scores.  Deterministic for a given batch.
+ */
+PA_API int pa_decode_masked(void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
+                            const void* v_cache, pa_dtype cache_dtype, const float* k_scale,
+                            const float* v_scale, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                            int num_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, float scale, float softcap, const float* alibi_slopes,
+                            const int32_t* kv_start, int window, const float* scores_in,
+                            float* scores_out, int score_stride, void* workspace,
+                            size_t workspace_bytes, int* err_flag, pa_stream_t stream);
+
+/* Workspace bytes of pa_decode_masked on the current device (score_width 0: no scores). */
+PA_API size_t pa_decode_masked_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                               int head_dim, int score_width);
+
+/*
+ * pa_prefill_masked -- pa_prefill with the changed scores of pa_decode_masked, row by
+ * row: row r of sequence s sits at pos = seq_lens[s] - q_len + r and sees the tokens
+ *   max(kv_start[row], pos - window + 1) <= t < max(pos + 1, min(prefix_lens[s], seq_lens[s])).
+ *
+ *   kv_start       int32 [total_q] or NULL (0): the first token of each row's document
+ *                  (packed documents); rows of one sequence may have any values.
+ *   prefix_lens    int32 [num_seqs] or NULL (0): the first prefix_lens[s] tokens are seen
+ *                  by every row of sequence s that its kv_start and window allow, later
+ *                  ones too (a prefix that attends in both directions).
+ *   softcap, alibi_slopes, window   as pa_decode_masked.
+ *   Other arguments as pa_prefill.  Also head_dim 64, fp32, and quantised caches (k_scale,
+ *   v_scale as pa_decode_v1), these on CUDA cores; num_heads / num_kv_heads <= 128.
+ *   A row that sees nothing gets zeros.  Unseen rows of K and V do not reach a row's
+ *   output, whatever they hold.  A sequence whose lengths or query rows are out of range
+ *   is skipped, a bad block id read as zeros, as in pa_prefill.
+ */
+PA_API int pa_prefill_masked(void* out, const void* q, pa_dtype q_dtype,
+                             const int32_t* query_start, int total_q, int max_query_len,
+                             const void* k_cache, const void* v_cache, pa_dtype cache_dtype,
+                             const float* k_scale, const float* v_scale,
+                             const int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* seq_lens, int num_seqs, int num_heads,
+                             int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                             float scale, float softcap, const float* alibi_slopes,
+                             const int32_t* kv_start, const int32_t* prefix_lens, int window,
+                             int* err_flag, pa_stream_t stream);
+
+/*
  * pa_evict -- cut cached sequences down to num_keep tokens by accumulated attention
  * weight: per (sequence, kv head) the num_recent newest tokens stay and, of the others,
  * the num_keep - num_recent with the highest scores (equal scores: the earlier token),

@@ -623,6 +623,132 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
   return cuda_status(e);
 }
 
+namespace {
+
+// Checks of the changed scores' own arguments.
+int check_scores(float scale, float softcap, const float* slopes, const int32_t* kv_start,
+                 int window) {
+  if (!std::isfinite(softcap) || softcap < 0.f || window < 0) return PA_ERR_INVALID_ARG;
+  if (softcap > 0.f && softcap < std::fabs(scale) * 0x1p-20f) return PA_ERR_INVALID_ARG;
+  if (!aligned(slopes, 4) || !aligned(kv_start, 4)) return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+}  // namespace
+
+PA_API size_t pa_decode_masked_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                               int head_dim, int score_width) {
+  if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || score_width < 0)
+    return 0;
+  return pa::masked_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim, score_width,
+                                    device_sms());
+}
+
+PA_API int pa_decode_masked(void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
+                            const void* v_cache, pa_dtype cache_dtype, const float* k_scale,
+                            const float* v_scale, const int32_t* block_tables,
+                            int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                            int num_heads, int num_kv_heads, int head_dim, int block_size,
+                            int num_blocks, float scale, float softcap, const float* alibi_slopes,
+                            const int32_t* kv_start, int window, const float* scores_in,
+                            float* scores_out, int score_stride, void* workspace,
+                            size_t workspace_bytes, int* err_flag, pa_stream_t stream) {
+  int rc = pa::fused_host_checks(out, q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale,
+                                 block_tables, max_blocks_per_seq, seq_lens, num_seqs, num_heads,
+                                 num_kv_heads, head_dim, block_size, num_blocks, scale);
+  if (rc != PA_OK) return rc;
+  rc = check_scores(scale, softcap, alibi_slopes, kv_start, window);
+  if (rc != PA_OK) return rc;
+  if (scores_in && !scores_out) return PA_ERR_INVALID_ARG;
+  if (scores_out && (score_stride <= 0 || !aligned(scores_out, 4) || !aligned(scores_in, 4)))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs > pa::kFusedMaxSeqs) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  const int sms = device_sms();
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < pa::masked_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                   scores_out ? score_stride : 0, sms))
+    return PA_ERR_INVALID_ARG;
+  pa::MaskedArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.slopes = alibi_slopes;
+  a.kv_start = kv_start;
+  a.scores_in = scores_in;
+  a.scores_out = scores_out;
+  a.err_flag = err_flag;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.window = window;
+  a.score_stride = score_stride;
+  a.scale = scale;
+  a.softcap = softcap;
+  return cuda_status(pa::launch_decode_masked(a, q_dtype, cache_dtype, head_dim, workspace, sms,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+PA_API int pa_prefill_masked(void* out, const void* q, pa_dtype q_dtype,
+                             const int32_t* query_start, int total_q, int max_query_len,
+                             const void* k_cache, const void* v_cache, pa_dtype cache_dtype,
+                             const float* k_scale, const float* v_scale,
+                             const int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* seq_lens, int num_seqs, int num_heads,
+                             int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                             float scale, float softcap, const float* alibi_slopes,
+                             const int32_t* kv_start, const int32_t* prefix_lens, int window,
+                             int* err_flag, pa_stream_t stream) {
+  if (num_kv_heads <= 0 || num_heads <= 0) return PA_ERR_INVALID_ARG;
+  // the group limit of the decode kernels does not hold here: check with one head a group
+  int rc = check_decode(q, q_dtype, k_cache, v_cache, cache_dtype, k_scale, v_scale, block_tables,
+                        max_blocks_per_seq, seq_lens, num_seqs, num_kv_heads, num_kv_heads,
+                        head_dim, block_size, num_blocks, scale);
+  if (rc != PA_OK) return rc;
+  if (num_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+  if (num_heads / num_kv_heads > 128) return PA_ERR_UNSUPPORTED;
+  rc = check_scores(scale, softcap, alibi_slopes, kv_start, window);
+  if (rc != PA_OK) return rc;
+  if (!out || !aligned(out, 16) || !query_start || !aligned(query_start, 4) ||
+      !aligned(prefix_lens, 4) || total_q < 0 || max_query_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_query_len == 0) return PA_OK;
+  pa::MaskedArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.query_start = query_start;
+  a.slopes = alibi_slopes;
+  a.kv_start = kv_start;
+  a.prefix_lens = prefix_lens;
+  a.err_flag = err_flag;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
+  a.total_q = total_q;
+  a.window = window;
+  a.scale = scale;
+  a.softcap = softcap;
+  return cuda_status(pa::launch_prefill_masked(a, q_dtype, cache_dtype, head_dim, max_query_len,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
 PA_API int pa_evict(void* k_cache, void* v_cache, pa_dtype cache_dtype, float* k_scale,
                     float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
                     const int32_t* seq_lens, const int32_t* new_block_tables, int max_new_blocks,

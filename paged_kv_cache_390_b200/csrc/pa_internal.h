@@ -144,6 +144,37 @@ struct EvictArgs {
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 
+// Attention with changed scores (pa_decode_masked, pa_prefill_masked).
+struct MaskedArgs {
+  void* out;                  // [rows, H, D] in q dtype
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start; // [S + 1]; null: one row per sequence (decode)
+  const float* slopes;        // [H] or null
+  const int32_t* kv_start;    // [rows] or null
+  const int32_t* prefix_lens; // [S] or null
+  const float* scores_in;     // [S, H_kv, score_stride] or null
+  float* scores_out;          // or null: no scores
+  float* lse;                 // workspace: [S, H], log2 units
+  float* logits;              // workspace: [S, H_kv, score_stride, G], log2 units
+  int* err_flag;
+  int max_blocks, num_seqs, num_heads, num_kv_heads, block_size, num_blocks, total_q;
+  int window, score_stride;
+  float scale, softcap;
+};
+
+size_t masked_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                              int score_width, int num_sms);
+cudaError_t launch_decode_masked(const MaskedArgs& a, int q_dtype, int cache_dtype, int head_dim,
+                                 void* workspace, int num_sms, cudaStream_t s);
+cudaError_t launch_prefill_masked(const MaskedArgs& a, int q_dtype, int cache_dtype, int head_dim,
+                                  int max_query_len, cudaStream_t s);
+
 // Persistent single-launch decode (pa_decode_fused): every warp streams an
 // equal contiguous range of the batch's 16-token tiles; a (sequence, kv head)
 // split between warps is merged by the warp that finishes it last.

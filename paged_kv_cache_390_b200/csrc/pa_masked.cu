@@ -1,0 +1,238 @@
+// pa_masked.cu -- paged attention with changed scores (pa_decode_masked,
+// pa_prefill_masked): per query row at position pos of its sequence
+//   x_t = cap * tanh(scale * q.K_t / cap)  (cap 0: scale * q.K_t)  - slope_h * |pos - t|
+// over the tokens lo <= t < hi that the row sees,
+//   lo = max(kv_start, pos - window + 1),  hi = min(len, max(pos + 1, prefix_len)),
+//   out = softmax(x) V; a row that sees nothing gets zeros.
+// pa_decode_masked also adds each cached token's weight, summed over the query heads of
+// its kv head, to a running score: the attention leaves its scores x in the workspace
+// and log-sum-exps beside them, and a second launch turns them into weights, so K is not
+// read twice.
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_tile.cuh"
+#include "pa_write.cuh"
+
+namespace pa {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Span {
+  int lo, hi;
+};
+
+__device__ __forceinline__ Span seen_span(int start, int pos, int window, int prefix, int len) {
+  Span s;
+  s.lo = max(start, 0);
+  if (window > 0) s.lo = max(s.lo, pos - window + 1);
+  s.hi = min(len, max(pos + 1, prefix));
+  return s;
+}
+
+template <typename KT, int NE>
+__device__ __forceinline__ void load_row(const void* cache, size_t row, float scale, int lane,
+                                         float (&x)[NE]) {
+#pragma unroll
+  for (int e = 0; e < NE; ++e) {
+    const size_t i = row + lane + 32 * e;
+    if constexpr (std::is_same<KT, int8_t>::value)
+      x[e] = static_cast<float>(static_cast<const int8_t*>(cache)[i]) * scale;
+    else if constexpr (std::is_same<KT, __nv_fp8_e4m3>::value)
+      x[e] = static_cast<float>(static_cast<const __nv_fp8_e4m3*>(cache)[i]) * scale;
+    else
+      x[e] = to_f32<KT>(static_cast<const KT*>(cache)[i]);
+  }
+}
+
+// One CTA per (query row, kv head, sequence); its warps take the group's query heads in
+// turn, lanes split head_dim, one token at a time.
+template <typename QT, typename KT, int D>
+__global__ void __launch_bounds__(256)
+    masked_rows_kernel(const __grid_constant__ MaskedArgs a) {
+  constexpr int NE = D / 32;
+  constexpr uint32_t FULL = 0xffffffffu;
+  constexpr bool QUANT = sizeof(KT) == 1;
+  const int r = blockIdx.x, kvh = blockIdx.y, s = blockIdx.z;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  const int G = a.num_heads / a.num_kv_heads, BS = a.block_size;
+  const bool prefill = a.query_start != nullptr;
+  griddep_launch_dependents();
+  griddep_wait();
+  int len = a.seq_lens[s];
+  const bool bad = len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_blocks) * BS;
+  int row = s, pos = len - 1;
+  if (prefill) {
+    const int q0 = a.query_start[s], n = a.query_start[s + 1] - q0;
+    if (bad || n < 0 || n > len || q0 < 0 || q0 > a.total_q - n) {
+      if (r == 0 && threadIdx.x == 0 && a.err_flag) report_error(a.err_flag, kErrSeqLen);
+      return;                                     // skipped
+    }
+    if (r >= n) return;
+    row = q0 + r;
+    pos = len - n + r;
+  } else if (bad && a.err_flag) {
+    if (threadIdx.x == 0) report_error(a.err_flag, kErrSeqLen);
+    len = 0;                                      // skipped: zeros
+    pos = -1;
+  }
+  const Span sp = seen_span(a.kv_start ? a.kv_start[row] : 0, pos, a.window,
+                            a.prefix_lens ? a.prefix_lens[s] : 0, len);
+  const int32_t* table = a.block_tables + static_cast<size_t>(s) * a.max_blocks;
+  for (int g = warp; g < G; g += nwarps) {
+    const int h = kvh * G + g;
+    const size_t qrow = (static_cast<size_t>(row) * a.num_heads + h) * D;
+    const float slope = a.slopes ? a.slopes[h] : 0.f;
+    float q[NE], acc[NE];
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      q[e] = to_f32<QT>(static_cast<const QT*>(a.q)[qrow + lane + 32 * e]);
+      acc[e] = 0.f;
+    }
+    float m2 = -INFINITY, l = 0.f;
+    for (int t = sp.lo; t < sp.hi; ++t) {
+      const int blk = table[t / BS];
+      bool zero = false;
+      float* lg = a.logits && t < a.score_stride
+                      ? a.logits + ((static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride + t) * G + g
+                      : nullptr;
+      if ((prefill || a.err_flag) && (blk < 0 || blk >= a.num_blocks)) {
+        if (lane == 0 && a.err_flag) report_error(a.err_flag, kErrBlockId);
+        if (!prefill) {                           // its tokens are dropped
+          if (lg && lane == 0) *lg = -INFINITY;
+          continue;
+        }
+        zero = true;                              // read as zeros
+      }
+      float k[NE], v[NE];
+      if (zero) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) k[e] = v[e] = 0.f;
+      } else {
+        const size_t at = ((static_cast<size_t>(blk) * BS + t % BS) * a.num_kv_heads + kvh) * D;
+        const size_t si = (static_cast<size_t>(blk) * a.num_kv_heads + kvh) * BS + t % BS;
+        load_row<KT, NE>(a.k_cache, at, QUANT ? a.k_scale[si] : 1.f, lane, k);
+        load_row<KT, NE>(a.v_cache, at, QUANT ? a.v_scale[si] : 1.f, lane, v);
+      }
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) x = fmaf(q[e], k[e], x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+      x *= a.scale;
+      if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
+      x = (x - slope * fabsf(static_cast<float>(pos - t))) * kLog2e;
+      if (lg && lane == 0) *lg = x;
+      const float mn = fmaxf(m2, x);
+      const float al = mn == -INFINITY ? 1.f : exp2f(m2 - mn);
+      const float p = mn == -INFINITY ? 0.f : exp2f(x - mn);
+      l = l * al + p;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) acc[e] = fmaf(p, v[e], acc[e] * al);
+      m2 = mn;
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays NaN
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const float o = acc[e] * inv;
+      if constexpr (std::is_same<QT, float>::value)
+        static_cast<float*>(a.out)[qrow + lane + 32 * e] = o;
+      else if constexpr (std::is_same<QT, __half>::value)
+        static_cast<__half*>(a.out)[qrow + lane + 32 * e] = __float2half_rn(o);
+      else
+        static_cast<__nv_bfloat16*>(a.out)[qrow + lane + 32 * e] = __float2bfloat16_rn(o);
+    }
+    if (a.lse && lane == 0)
+      a.lse[static_cast<size_t>(s) * a.num_heads + h] = l == 0.f ? -INFINITY : m2 + log2f(l);
+  }
+}
+
+// scores_out[s, kvh, t] = scores_in + sum over the group of 2^(x - lse): one thread per
+// (token, kv head, sequence).
+__global__ void __launch_bounds__(256)
+    masked_scores_kernel(const __grid_constant__ MaskedArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int t = blockIdx.x * 256 + threadIdx.x, kvh = blockIdx.y, s = blockIdx.z;
+  int len = a.seq_lens[s];
+  if (len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_blocks) * a.block_size)
+    return;                                       // a skipped sequence keeps its scores
+  if (t >= min(len, a.score_stride)) return;
+  const int G = a.num_heads / a.num_kv_heads;
+  const Span sp = seen_span(a.kv_start ? a.kv_start[s] : 0, len - 1, a.window, 0, len);
+  const size_t i = (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride + t;
+  float w = 0.f;
+  if (t >= sp.lo && t < sp.hi) {
+    for (int g = 0; g < G; ++g) {
+      const float lse = a.lse[static_cast<size_t>(s) * a.num_heads + kvh * G + g];
+      if (lse != -INFINITY) w += exp2f(a.logits[i * G + g] - lse);
+    }
+  }
+  a.scores_out[i] = (a.scores_in ? a.scores_in[i] : 0.f) + w;
+}
+
+template <typename QT, typename KT>
+cudaError_t launch_rows(const MaskedArgs& a, int D, int rows, cudaStream_t s) {
+  const int G = a.num_heads / a.num_kv_heads;
+  const dim3 grid(rows, a.num_kv_heads, a.num_seqs), block(32 * (G < 8 ? G : 8));
+  const bool pdl = pdl_mode() != 0;
+  return D == 128 ? launch_kernel(masked_rows_kernel<QT, KT, 128>, grid, block, 0, s, pdl, a)
+                  : launch_kernel(masked_rows_kernel<QT, KT, 64>, grid, block, 0, s, pdl, a);
+}
+
+template <typename QT>
+cudaError_t launch_q(const MaskedArgs& a, int cache_dtype, int D, int rows, cudaStream_t s) {
+  if (cache_dtype == PA_INT8) return launch_rows<QT, int8_t>(a, D, rows, s);
+  if (cache_dtype == PA_FP8E4M3) return launch_rows<QT, __nv_fp8_e4m3>(a, D, rows, s);
+  return launch_rows<QT, QT>(a, D, rows, s);
+}
+
+cudaError_t launch_attention(const MaskedArgs& a, int q_dtype, int cache_dtype, int D, int rows,
+                             cudaStream_t s) {
+  switch (q_dtype) {
+    case PA_F32: return launch_rows<float, float>(a, D, rows, s);
+    case PA_F16: return launch_q<__half>(a, cache_dtype, D, rows, s);
+    case PA_BF16: return launch_q<__nv_bfloat16>(a, cache_dtype, D, rows, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+namespace {
+size_t lse_bytes(int num_seqs, int num_heads) {
+  return (static_cast<size_t>(num_seqs) * num_heads * sizeof(float) + 255) / 256 * 256;
+}
+}  // namespace
+
+// The persistent decode's workspace, then lse, then the scores x of every cached token.
+size_t masked_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                              int score_width, int num_sms) {
+  return fused_workspace_bytes(num_seqs, num_kv_heads, head_dim, num_sms) +
+         lse_bytes(num_seqs, num_heads) +
+         static_cast<size_t>(num_seqs) * num_heads * score_width * sizeof(float);
+}
+
+cudaError_t launch_decode_masked(const MaskedArgs& a0, int q_dtype, int cache_dtype, int head_dim,
+                                 void* workspace, int num_sms, cudaStream_t s) {
+  MaskedArgs a = a0;
+  if (a.scores_out) {
+    char* ws = static_cast<char*>(workspace) +
+               fused_workspace_bytes(a.num_seqs, a.num_kv_heads, head_dim, num_sms);
+    a.lse = reinterpret_cast<float*>(ws);
+    a.logits = reinterpret_cast<float*>(ws + lse_bytes(a.num_seqs, a.num_heads));
+  }
+  cudaError_t e = launch_attention(a, q_dtype, cache_dtype, head_dim, 1, s);
+  if (e != cudaSuccess || !a.scores_out) return e;
+  const long long cap = static_cast<long long>(a.max_blocks) * a.block_size;
+  const int width = static_cast<int>(cap < a.score_stride ? cap : a.score_stride);
+  return launch_kernel(masked_scores_kernel, dim3((width + 255) / 256, a.num_kv_heads, a.num_seqs),
+                       dim3(256), 0, s, pdl_mode() != 0, a);
+}
+
+cudaError_t launch_prefill_masked(const MaskedArgs& a, int q_dtype, int cache_dtype, int head_dim,
+                                  int max_query_len, cudaStream_t s) {
+  return launch_attention(a, q_dtype, cache_dtype, head_dim, max_query_len, s);
+}
+
+}  // namespace pa

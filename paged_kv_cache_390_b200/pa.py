@@ -80,6 +80,11 @@ def lib() -> ctypes.CDLL:
             "pa_prefill": (I, [P, P, I, P, I, I, P, P, I, P, I, P, I, I, I, I, I, I, F, P, P]),
             "pa_rope_and_cache": (I, [P, P, P, P, I, LL, LL, LL, P, I, P, P, I, I, P, P, I, P, P,
                                       P, I, I, I, I, I, I, P, P]),
+            "pa_decode_masked": (I, [P, P, I, P, P, I, P, P, P, I, P, I, I, I, I, I, I, F, F, P, P,
+                                     I, P, P, I, P, S, P, P]),
+            "pa_decode_masked_workspace_bytes": (S, [I, I, I, I, I]),
+            "pa_prefill_masked": (I, [P, P, I, P, I, I, P, P, I, P, P, P, I, P, I, I, I, I, I, I, F,
+                                      F, P, P, P, I, P, P]),
             "pa_evict": (I, [P, P, I, P, P, P, I, P, P, I, P, I, I, I, P, I, P, I, P, I, I, I, I, I,
                              P, P]),
         }
@@ -284,6 +289,113 @@ def copy_blocks(src_k, src_v, dst_k, dst_v, block_mapping, *, cache_dtype=None,
         block_mapping.shape[0] if block_mapping.numel() else 0, num_kv_heads, head_dim,
         block_size, _ptr(err_flag), _stream(stream))
     _check(rc, "pa_copy_blocks")
+
+
+class MaskedWorkspace:
+    """Workspace of pa_decode_masked, zeroed once; score_width is the scores' last
+    dimension (0: calls without scores)."""
+
+    def __init__(self, num_seqs, num_heads, num_kv_heads, head_dim, score_width=0, device="cuda"):
+        dev = torch.device(device)
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.device(dev):
+            self.nbytes = int(lib().pa_decode_masked_workspace_bytes(
+                num_seqs, num_heads, num_kv_heads, head_dim, score_width))
+            self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+
+
+def _row_ints(t, n, what):
+    if t is not None and (t.dtype != torch.int32 or t.shape != (n,)):
+        raise ValueError(f"{what} must be int32 [{n}]")
+
+
+def _mask_checks(q, head_dim, num_kv_heads, slopes):
+    num_heads = q.shape[1]
+    if q.dim() != 3 or q.shape[2] != head_dim or num_heads % num_kv_heads:
+        raise ValueError("q must be [rows, num_heads, head_dim], whole groups of heads")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (num_heads,)):
+        raise ValueError("alibi_slopes must be float32 [num_heads]")
+
+
+def decode_masked(q, k_cache, v_cache, block_tables, seq_lens, scale, *, softcap=0.0,
+                  alibi_slopes=None, kv_start=None, window=0, scores_in=None, scores_out=None,
+                  out=None, workspace: MaskedWorkspace | None = None, cache_dtype=None,
+                  k_scale=None, v_scale=None, err_flag=None, stream=None) -> torch.Tensor:
+    """Paged decode attention with scores capped by a tanh (softcap), a bias by distance
+    (alibi_slopes float32 [H]), the start of the token's document (kv_start int32 [S]) and
+    a sliding window; with scores_out (float32 [S, H_kv, width]) every cached token's
+    weight, summed over its kv head's query heads, is added to scores_in."""
+    num_blocks, block_size, num_kv_heads, head_dim = k_cache.shape
+    num_seqs, num_heads, _ = q.shape
+    code = _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype)
+    _mask_checks(q, head_dim, num_kv_heads, alibi_slopes)
+    _batch_checks(block_tables, seq_lens, num_seqs)
+    _row_ints(kv_start, num_seqs, "kv_start")
+    width = 0
+    if scores_out is not None:
+        width = scores_out.shape[-1]
+        for t in (scores_in, scores_out):
+            if t is not None and (t.dtype != torch.float32
+                                  or t.shape != (num_seqs, num_kv_heads, width)):
+                raise ValueError("scores must be float32 [num_seqs, num_kv_heads, width]")
+    elif scores_in is not None:
+        raise ValueError("scores_in needs scores_out")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
+        raise ValueError("out must have q's shape and dtype")
+    dev = _same_device(q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes, kv_start,
+                       scores_in, scores_out, out, k_scale, v_scale, err_flag,
+                       workspace.buf if workspace is not None else None)
+    with _on(dev, stream) as s:
+        if workspace is None:
+            workspace = MaskedWorkspace(num_seqs, num_heads, num_kv_heads, head_dim, width, dev)
+        if out is None:
+            out = torch.empty_like(q)
+        rc = lib().pa_decode_masked(
+            _ptr(out), _ptr(q), _FLOAT_CODES[q.dtype], _ptr(k_cache), _ptr(v_cache), code,
+            _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+            _ptr(seq_lens), num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+            float(scale), float(softcap), _ptr(alibi_slopes), _ptr(kv_start), int(window),
+            _ptr(scores_in), _ptr(scores_out), width, _ptr(workspace.buf), workspace.nbytes,
+            _ptr(err_flag), s)
+    _check(rc, "pa_decode_masked")
+    return out
+
+
+def prefill_masked(q, k_cache, v_cache, block_tables, seq_lens, query_start, scale, *,
+                   softcap=0.0, alibi_slopes=None, kv_start=None, prefix_lens=None, window=0,
+                   max_query_len=None, out=None, cache_dtype=None, k_scale=None, v_scale=None,
+                   err_flag=None, stream=None) -> torch.Tensor:
+    """pa_prefill with changed scores: as decode_masked, with a document start per query
+    row (kv_start int32 [total_q]) and a prefix that every row of its sequence sees
+    (prefix_lens int32 [S])."""
+    num_blocks, block_size, num_kv_heads, head_dim = k_cache.shape
+    total_q, num_heads, _ = q.shape
+    num_seqs = seq_lens.shape[0]
+    code = _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype)
+    _mask_checks(q, head_dim, num_kv_heads, alibi_slopes)
+    _batch_checks(block_tables, seq_lens, num_seqs)
+    _row_ints(query_start, num_seqs + 1, "query_start")
+    _row_ints(kv_start, total_q, "kv_start")
+    _row_ints(prefix_lens, num_seqs, "prefix_lens")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
+        raise ValueError("out must have q's shape and dtype")
+    dev = _same_device(q, k_cache, v_cache, block_tables, seq_lens, query_start, alibi_slopes,
+                       kv_start, prefix_lens, out, k_scale, v_scale, err_flag)
+    with _on(dev, stream) as s:
+        if max_query_len is None:
+            max_query_len = (int((query_start[1:] - query_start[:-1]).max())
+                             if query_start.numel() > 1 else 0)
+        if out is None:
+            out = torch.empty_like(q)
+        rc = lib().pa_prefill_masked(
+            _ptr(out), _ptr(q), _FLOAT_CODES[q.dtype], _ptr(query_start), total_q,
+            int(max_query_len), _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), num_seqs, num_heads,
+            num_kv_heads, head_dim, block_size, num_blocks, float(scale), float(softcap),
+            _ptr(alibi_slopes), _ptr(kv_start), _ptr(prefix_lens), int(window), _ptr(err_flag), s)
+    _check(rc, "pa_prefill_masked")
+    return out
 
 
 def evict(k_cache, v_cache, block_tables, seq_lens, new_block_tables, scores, num_keep, num_recent,

@@ -56,3 +56,64 @@ def evict(scores, lens, num_keep, num_recent):
             per.append(sorted(new + old[:m - len(new)]))
         out.append(per)
     return out
+
+
+# ---------------------------------------------------------------------- attention
+
+def attend(q, k, v, scale, lo, hi, pos, softcap=0.0, slopes=None):
+    """One sequence, rows of one call: q [R, H, D], k, v [n, Hkv, D] (64-bit values), lo, hi,
+    pos per row.  Only seen tokens enter (unseen ones may hold anything).  Returns out
+    [R, H, D], weights [R, H, n], bound terms: dx [R, H] (how far a score may be off in
+    32-bit arithmetic) and wv [R, H, D] = sum w |v|."""
+    R, H, D = q.shape
+    n, Hkv, _ = k.shape
+    G = H // Hkv
+    out, w = torch.zeros(R, H, D, dtype=torch.float64), torch.zeros(R, H, n, dtype=torch.float64)
+    dx, wv = torch.zeros(R, H, dtype=torch.float64), torch.zeros(R, H, D, dtype=torch.float64)
+    q = q.double()
+    for r in range(R):
+        a, b = int(lo[r]), int(hi[r])
+        if a >= b:
+            continue
+        kk = k[a:b].repeat_interleave(G, dim=1)                 # [m, H, D]
+        vv = v[a:b].repeat_interleave(G, dim=1)
+        x = torch.einsum("hd,mhd->hm", q[r], kk) * scale
+        size = torch.einsum("hd,mhd->hm", q[r].abs(), kk.abs()) * abs(scale)
+        if softcap:
+            x = softcap * torch.tanh(x / softcap)
+        bias = torch.zeros_like(x)
+        if slopes is not None:
+            dist = (int(pos[r]) - torch.arange(a, b)).abs().double()
+            bias = slopes.double()[:, None] * dist
+        x = x - bias
+        p = torch.softmax(x, dim=1)
+        w[r, :, a:b] = p
+        out[r] = torch.einsum("hm,mhd->hd", p, vv)
+        wv[r] = torch.einsum("hm,mhd->hd", p, vv.abs())
+        # D products summed (each step to 2 ulp: matrix units may truncate), the cap's tanh
+        # to 4 ulp of the cap, the bias to 2, and 8 more on the score and exponent itself;
+        # only tokens whose weight counts (a score off by e moves its weight by w * e)
+        off = 2.0 ** -23 * ((D + 8) * size + 4 * softcap + 2 * bias + 8 * (x.abs() + 1))
+        dx[r] = torch.where(p > 2.0 ** -30, off, torch.zeros_like(off)).amax(1)
+    return out, w, dx, wv
+
+
+def attention_tol(out, dx, wv, dt, cache, n, vmax, smax=0.0):
+    """Elementwise bound on an attention output: half a step of dt; scores off by dx move
+    every weight and the sum by a factor exp(+-dx) each (2 dx); the running sums' 32-bit
+    rescaling, 2^-18; P in 16 bits: fp16 half a step 2^-11 and 2^-25 absolute below
+    its normal range (n tokens), bf16 as two parts 2^-16; INT8 under fp16: codes enter
+    as 1152 + c, whose sum is held in 32 bits (n / 16 + 8 roundings)."""
+    p_err = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -16, torch.float32: 0.0}[dt]
+    tol = half_step(dt) * out.abs() * (1 + 2.0 ** -9) + (p_err + 2 * dx[..., None] + 2.0 ** -18) * wv
+    tol = tol + n * 2.0 ** -25 * vmax
+    if cache == "int8" and dt == torch.float16:
+        tol = tol + (n / 16 + 8) * 2.0 ** -24 * 1152 * smax
+    return tol + 2.0 ** -24 * torch.finfo(dt).smallest_normal
+
+
+def scores_tol(scores, w_sum, dx):
+    """Bound on running scores [.., n]: w off by a factor exp(2 dx) and 2^-19 (exponentials
+    and log-sum-exp in 32 bits), one rounding of the sum over the group and one of the
+    total."""
+    return w_sum * (2 * dx + 2.0 ** -19) + 2.0 ** -23 * scores.abs() + 2.0 ** -40
