@@ -693,6 +693,8 @@ PA_API int pa_decode_masked(void* out, const void* q, pa_dtype q_dtype, const vo
   a.score_stride = score_stride;
   a.scale = scale;
   a.softcap = softcap;
+  a.timeout_ns = wait_limit();
+  a.inject = g_inject.load(std::memory_order_relaxed);
   return cuda_status(pa::launch_decode_masked(a, q_dtype, cache_dtype, head_dim, workspace, sms,
                                               reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -745,6 +747,8 @@ PA_API int pa_prefill_masked(void* out, const void* q, pa_dtype q_dtype,
   a.window = window;
   a.scale = scale;
   a.softcap = softcap;
+  a.timeout_ns = wait_limit();
+  a.inject = g_inject.load(std::memory_order_relaxed);
   return cuda_status(pa::launch_prefill_masked(a, q_dtype, cache_dtype, head_dim, max_query_len,
                                                reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -166,6 +166,8 @@ struct MaskedArgs {
   int max_blocks, num_seqs, num_heads, num_kv_heads, block_size, num_blocks, total_q;
   int window, score_stride;
   float scale, softcap;
+  unsigned long long timeout_ns;
+  int inject;
 };
 
 size_t masked_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
@@ -215,10 +217,25 @@ struct FusedArgs {
   int* done;                    // PDL mode 3: CTA exit counter, zero on entry, left zero
   int sm_limit;                 // > 0: a grid for this many SMs only (the others are busy
                                 // with a launch this one runs beside); 0: every SM
+  // Changed scores (pa_decode_masked; the MASK build only).
+  const float* slopes;          // [H] or null
+  const int32_t* kv_start;      // [S] or null
+  float cap_in;                 // scale / softcap (0: no cap)
+  float cap_log2;               // softcap * log2(e)
+  int window;                   // 0: no limit
+  float* lse;                   // [S, H] log2 units, or null: no running scores
+  float* logits;                // [S, H_kv, score_stride, G] log2 units
+  int score_stride;
   int ctas_per_sm;              // 3 (16-bit cache, head_dim 128): the build capped at 168
                                 // registers, three CTAs per SM; other > 0: at most this
                                 // many CTAs per SM; 0: as many as fit
 };
+
+// Arrival counters at the head of the persistent decode's workspace.
+inline size_t fused_counter_bytes(int num_seqs, int num_kv_heads) {
+  const size_t b = static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(int);
+  return (b + 255) / 256 * 256;
+}
 
 // Floats of one partial record (padded to whole 128-byte lines).
 inline int fused_record_floats(int head_dim) { return 8 * head_dim + 32; }
@@ -278,7 +295,18 @@ struct PrefillArgs {
   float* part_o;              // [rows, H, D]
   float* part_m;              // [rows, H], log2 domain (scale folded in)
   float* part_l;              // [rows, H]
+  // Changed scores (pa_prefill_masked; its builds of the kernel only).
+  const float* slopes;        // [H] or null
+  const int32_t* kv_start;    // [total_q] or null
+  const int32_t* prefix_lens; // [num_seqs] or null
+  float cap_in;               // scale / softcap (0: no cap)
+  float cap_log2;             // softcap * log2(e)
+  int window, total_q, block_size;
 };
+
+// pa_prefill_masked on the tensor cores: 16-bit q and caches, head_dim 128.
+cudaError_t launch_prefill_masked_tc(const PrefillArgs& a, int q_dtype, int max_query_len,
+                                     cudaStream_t s);
 
 // allow_pdl = false launches without the programmatic-dependent-launch attribute
 // even when it is on: the CTAs are placed on an idle GPU instead of on whichever

@@ -8,27 +8,11 @@
 // its kv head, to a running score: the attention leaves its scores x in the workspace
 // and log-sum-exps beside them, and a second launch turns them into weights, so K is not
 // read twice.
-#include "pa_device.cuh"
-#include "pa_internal.h"
-#include "pa_tile.cuh"
+#include "pa_fused_kernel.cuh"
 #include "pa_write.cuh"
 
 namespace pa {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct Span {
-  int lo, hi;
-};
-
-__device__ __forceinline__ Span seen_span(int start, int pos, int window, int prefix, int len) {
-  Span s;
-  s.lo = max(start, 0);
-  if (window > 0) s.lo = max(s.lo, pos - window + 1);
-  s.hi = min(len, max(pos + 1, prefix));
-  return s;
-}
 
 template <typename KT, int NE>
 __device__ __forceinline__ void load_row(const void* cache, size_t row, float scale, int lane,
@@ -200,6 +184,37 @@ cudaError_t launch_attention(const MaskedArgs& a, int q_dtype, int cache_dtype, 
 }  // namespace
 
 namespace {
+
+template <typename QT, int KIND>
+cudaError_t masked_shape(const FusedArgs& a, int D, int BS, size_t ws, cudaStream_t s) {
+#define PA_CASE(DD, BB) \
+  if (D == DD && BS == BB) return launch_fused_t<QT, KIND, DD, BB, true>(a, ws, s);
+  PA_CASE(128, 16)
+  PA_CASE(128, 8)
+  PA_CASE(128, 32)
+  PA_CASE(64, 16)
+  PA_CASE(64, 8)
+  PA_CASE(64, 32)
+#undef PA_CASE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_masked_fused(const FusedArgs& a, int q_dtype, int cache_dtype, int D, int BS,
+                                size_t ws, cudaStream_t s) {
+  const bool qh = q_dtype == PA_F16;
+  switch (cache_dtype) {
+    case PA_F16: return masked_shape<__half, kKind16>(a, D, BS, ws, s);
+    case PA_BF16: return masked_shape<__nv_bfloat16, kKind16>(a, D, BS, ws, s);
+    case PA_INT8:
+      return qh ? masked_shape<__half, kKindI8>(a, D, BS, ws, s)
+                : masked_shape<__nv_bfloat16, kKindI8>(a, D, BS, ws, s);
+    case PA_FP8E4M3:
+      return qh ? masked_shape<__half, kKindE4M3>(a, D, BS, ws, s)
+                : masked_shape<__nv_bfloat16, kKindE4M3>(a, D, BS, ws, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
 size_t lse_bytes(int num_seqs, int num_heads) {
   return (static_cast<size_t>(num_seqs) * num_heads * sizeof(float) + 255) / 256 * 256;
 }
@@ -222,7 +237,42 @@ cudaError_t launch_decode_masked(const MaskedArgs& a0, int q_dtype, int cache_dt
     a.lse = reinterpret_cast<float*>(ws);
     a.logits = reinterpret_cast<float*>(ws + lse_bytes(a.num_seqs, a.num_heads));
   }
-  cudaError_t e = launch_attention(a, q_dtype, cache_dtype, head_dim, 1, s);
+  cudaError_t e;
+  if (cache_dtype == PA_F32) {
+    e = launch_rows<float, float>(a, head_dim, 1, s);
+  } else {
+    FusedArgs f{};
+    f.out = a.out;
+    f.q = a.q;
+    f.k_cache = a.k_cache;
+    f.v_cache = a.v_cache;
+    f.k_scale = a.k_scale;
+    f.v_scale = a.v_scale;
+    f.block_tables = a.block_tables;
+    f.seq_lens = a.seq_lens;
+    f.err_flag = a.err_flag;
+    f.counters = static_cast<int*>(workspace);
+    f.max_blocks = a.max_blocks;
+    f.num_seqs = a.num_seqs;
+    f.num_heads = a.num_heads;
+    f.num_kv_heads = a.num_kv_heads;
+    f.num_blocks = a.num_blocks;
+    f.stages = 2;
+    f.scale_log2 = a.scale * kLog2e;
+    f.timeout_ns = a.timeout_ns;
+    f.inject = a.inject;
+    f.pdl = pdl_mode() != 0 ? 1 : 0;         // kv_start is read with the lengths: after the wait
+    f.slopes = a.slopes;
+    f.kv_start = a.kv_start;
+    f.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+    f.cap_log2 = a.softcap * kLog2e;
+    f.window = a.window;
+    f.lse = a.lse;
+    f.logits = a.logits;
+    f.score_stride = a.score_stride;
+    e = launch_masked_fused(f, q_dtype, cache_dtype, head_dim, a.block_size,
+                            fused_workspace_bytes(a.num_seqs, a.num_kv_heads, head_dim, num_sms), s);
+  }
   if (e != cudaSuccess || !a.scores_out) return e;
   const long long cap = static_cast<long long>(a.max_blocks) * a.block_size;
   const int width = static_cast<int>(cap < a.score_stride ? cap : a.score_stride);
@@ -232,7 +282,34 @@ cudaError_t launch_decode_masked(const MaskedArgs& a0, int q_dtype, int cache_dt
 
 cudaError_t launch_prefill_masked(const MaskedArgs& a, int q_dtype, int cache_dtype, int head_dim,
                                   int max_query_len, cudaStream_t s) {
-  return launch_attention(a, q_dtype, cache_dtype, head_dim, max_query_len, s);
+  if (head_dim != 128 || cache_dtype != q_dtype || q_dtype == PA_F32)
+    return launch_attention(a, q_dtype, cache_dtype, head_dim, max_query_len, s);
+  PrefillArgs p{};
+  p.out = a.out;
+  p.q = a.q;
+  p.k_cache = a.k_cache;
+  p.v_cache = a.v_cache;
+  p.block_tables = a.block_tables;
+  p.seq_lens = a.seq_lens;
+  p.query_start = a.query_start;
+  p.err_flag = a.err_flag;
+  p.max_blocks = a.max_blocks;
+  p.num_seqs = a.num_seqs;
+  p.num_heads = a.num_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.num_blocks = a.num_blocks;
+  p.scale_log2 = a.scale * kLog2e;
+  p.timeout_ns = a.timeout_ns;
+  p.inject = a.inject;
+  p.slopes = a.slopes;
+  p.kv_start = a.kv_start;
+  p.prefix_lens = a.prefix_lens;
+  p.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+  p.cap_log2 = a.softcap * kLog2e;
+  p.window = a.window;
+  p.total_q = a.total_q;
+  p.block_size = a.block_size;
+  return launch_prefill_masked_tc(p, q_dtype, max_query_len, s);
 }
 
 }  // namespace pa

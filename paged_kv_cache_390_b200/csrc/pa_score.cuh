@@ -1,0 +1,47 @@
+// pa_score.cuh -- the changed scores of pa_decode_masked / pa_prefill_masked: the tanh cap,
+// the bias by distance and the span of tokens a query row sees.
+#pragma once
+
+#include <stdint.h>
+
+namespace pa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Tokens [lo, hi) that a row at position pos sees.
+struct Span {
+  int lo, hi;
+};
+
+__device__ __forceinline__ Span seen_span(int start, int pos, int window, int prefix, int len) {
+  Span s;
+  s.lo = max(start, 0);
+  if (window > 0) s.lo = max(s.lo, pos - window + 1);
+  s.hi = min(len, max(pos + 1, prefix));
+  return s;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(y) to ~2 ulp.  Below 0.625 an odd polynomial y + y z Q(z), z = y^2, with Q of
+// degree 4 interpolating (tanh(y) / y - 1) / z at the Chebyshev points of [0, 0.625^2]
+// (2e-8 relative); above, 1 - 2 / (1 + e^(2|y|)), whose error is absolute (2^-23) and so
+// relative there.  (Near 0 that form alone would lose the digits of a small score, and
+// a score carries into its weight absolutely: cap 50 would leave 1e-5 on every weight.)
+__device__ __forceinline__ float tanh_f32(float y) {
+  const float a = fabsf(y), z = y * y;
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * (2.f * kLog2e)));
+  const float big = copysignf(fmaf(-2.f, rcp_approx(e + 1.f), 1.f), y);
+  float q = fmaf(z, -0.006096714176237583f, 0.020997179672122f);
+  q = fmaf(z, q, -0.05385090783238411f);
+  q = fmaf(z, q, 0.1333276927471161f);
+  q = fmaf(z, q, -0.333333283662796f);
+  return a < 0.625f ? fmaf(y * z, q, y) : big;
+}
+
+}  // namespace pa

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_score.cuh"
 
 namespace pa {
 
@@ -222,18 +223,30 @@ __device__ __forceinline__ void load_tile(TileFrag<KIND, D, BS>& f, uint32_t st,
   }
 }
 
+// Changed scores of a tile (pa_decode_masked).  Row i of the tile is token t0 + i.
+struct ScoreMod {
+  float cap_in, cap_log2;           // scale / cap, cap * log2(e); cap_in 0: no cap
+  float slope[2];                   // per query head 2c, 2c + 1, times log2(e)
+  int back;                         // the query's position - t0
+  int lo;                           // first seen row (may be negative)
+  int G;                            // query heads per kv head
+  int room;                         // rows whose scores are kept
+  float* logits;                    // null, or the scores of row 0: [row][G], log2 units
+};
+
 // Accumulate one tile into `w`.  nv = valid tokens of the tile (from its
 // start), okm = bit b set if box b was loaded (tokens of other boxes masked).
-template <typename QT, int KIND, int D, int BS>
+template <typename QT, int KIND, int D, int BS, bool MASK = false>
 __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
                                              const TileFrag<KIND, D, BS>& f, int nv, int okm,
-                                             float scale_log2, int lane) {
+                                             float scale_log2, int lane,
+                                             const ScoreMod& mod = ScoreMod()) {
   using T = Tr<KIND, D, BS>;
   constexpr uint32_t FULL = 0xffffffffu;
   const int r = lane >> 2, c = lane & 3;
   const int tok0 = tau<T::ROWB>(r), tok1 = tok0 + 8;
   const int ta = tau<T::ROWB>(2 * c), tb = tau<T::ROWB>(2 * c + 1);
-  const bool partial = (nv < 16) || (okm != (1 << T::NBOX) - 1);
+  const bool partial = (nv < 16) || (okm != (1 << T::NBOX) - 1) || (MASK && mod.lo > 0);
 
   // ---- S^T = K Q^T, two independent accumulator chains
   float acc0[4] = {0.f, 0.f, 0.f, 0.f}, acc1[4] = {0.f, 0.f, 0.f, 0.f};
@@ -275,13 +288,50 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
       else mma_16816<QT>(acc0, af, w.qf[ks][0], w.qf[ks][1]);
     }
   }
-  const bool ok0 = tok0 < nv && ((okm >> (tok0 / T::BOXH)) & 1);
-  const bool ok1 = tok1 < nv && ((okm >> (tok1 / T::BOXH)) & 1);
-  const float s0 = scale_log2 * f.ks0, s1 = scale_log2 * f.ks1;
-  float x0 = ok0 ? (acc0[0] + acc1[0]) * s0 : -INFINITY;
-  float x1 = ok0 ? (acc0[1] + acc1[1]) * s0 : -INFINITY;
-  float x2 = ok1 ? (acc0[2] + acc1[2]) * s1 : -INFINITY;
-  float x3 = ok1 ? (acc0[3] + acc1[3]) * s1 : -INFINITY;
+  const bool ok0 = tok0 < nv && ((okm >> (tok0 / T::BOXH)) & 1) && (!MASK || tok0 >= mod.lo);
+  const bool ok1 = tok1 < nv && ((okm >> (tok1 / T::BOXH)) & 1) && (!MASK || tok1 >= mod.lo);
+  float x0, x1, x2, x3;
+  if constexpr (MASK) {
+    x0 = acc0[0] + acc1[0];
+    x1 = acc0[1] + acc1[1];
+    x2 = acc0[2] + acc1[2];
+    x3 = acc0[3] + acc1[3];
+    if (mod.cap_in != 0.f) {
+      const float s0 = mod.cap_in * f.ks0, s1 = mod.cap_in * f.ks1;
+      x0 = mod.cap_log2 * tanh_f32(x0 * s0);
+      x1 = mod.cap_log2 * tanh_f32(x1 * s0);
+      x2 = mod.cap_log2 * tanh_f32(x2 * s1);
+      x3 = mod.cap_log2 * tanh_f32(x3 * s1);
+    } else {
+      const float s0 = scale_log2 * f.ks0, s1 = scale_log2 * f.ks1;
+      x0 *= s0;
+      x1 *= s0;
+      x2 *= s1;
+      x3 *= s1;
+    }
+    const float d0 = static_cast<float>(tok0 - mod.back), d1 = static_cast<float>(tok1 - mod.back);
+    x0 = ok0 ? fmaf(mod.slope[0], d0, x0) : -INFINITY;
+    x1 = ok0 ? fmaf(mod.slope[1], d0, x1) : -INFINITY;
+    x2 = ok1 ? fmaf(mod.slope[0], d1, x2) : -INFINITY;
+    x3 = ok1 ? fmaf(mod.slope[1], d1, x3) : -INFINITY;
+    if (mod.logits) {                          // dropped rows' too (-inf); not past the end
+      const int keep = min(nv, mod.room), g = 2 * c, G = mod.G;
+      if (g < G) {
+        if (tok0 < keep) mod.logits[tok0 * G + g] = x0;
+        if (tok1 < keep) mod.logits[tok1 * G + g] = x2;
+        if (g + 1 < G) {
+          if (tok0 < keep) mod.logits[tok0 * G + g + 1] = x1;
+          if (tok1 < keep) mod.logits[tok1 * G + g + 1] = x3;
+        }
+      }
+    }
+  } else {
+    const float s0 = scale_log2 * f.ks0, s1 = scale_log2 * f.ks1;
+    x0 = ok0 ? (acc0[0] + acc1[0]) * s0 : -INFINITY;
+    x1 = ok0 ? (acc0[1] + acc1[1]) * s0 : -INFINITY;
+    x2 = ok1 ? (acc0[2] + acc1[2]) * s1 : -INFINITY;
+    x3 = ok1 ? (acc0[3] + acc1[3]) * s1 : -INFINITY;
+  }
 
   // ---- online softmax (per query head g = 2c, 2c+1)
   float tm0 = fmaxf(x0, x2), tm1 = fmaxf(x1, x3);
@@ -327,8 +377,10 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   }
   // P as the B operand.  bf16 keeps 8 significant bits, so P is split into a
   // high and a low bf16 part (two MMAs, ~16 bits); fp16's 11 bits (P in [0, 1])
-  // keep the output within the comparison bound with one MMA.
-  constexpr bool kSplitP = std::is_same<QT, __nv_bfloat16>::value;
+  // keep the output within the comparison bound with one MMA.  MASK splits fp16 too:
+  // one fp16 part alone is as far off as the output's own rounding (a short INT8
+  // batch: 3.3e-4 against 2.1e-4 relative from the rounding alone).
+  constexpr bool kSplitP = MASK || std::is_same<QT, __nv_bfloat16>::value;
   const uint32_t h01 = pack2<QT>(p0, p1), h23 = pack2<QT>(p2, p3);
   const float2 f01 = unpack2<QT>(h01), f23 = unpack2<QT>(h23);
   const uint32_t l01 = pack2<QT>(p0 - f01.x, p1 - f01.y);
@@ -339,11 +391,18 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
     // the sum of the P' the MMAs see (fp16-rounded), for the bias of the codes
     w.lv[0] += f01.x + f23.x;
     w.lv[1] += f01.y + f23.y;
+    if constexpr (kSplitP) {
+      const float2 e01 = unpack2<QT>(l01), e23 = unpack2<QT>(l23);
+      w.lv[0] += e01.x + e23.x;
+      w.lv[1] += e01.y + e23.y;
+    }
   }
 
   uint32_t mk01 = ~0u, mk23 = ~0u;
   if (partial) {
-    auto valid = [&](int t) { return t < nv && ((okm >> (t / T::BOXH)) & 1); };
+    auto valid = [&](int t) {
+      return t < nv && ((okm >> (t / T::BOXH)) & 1) && (!MASK || t >= mod.lo);
+    };
     mk01 = (valid(ta) ? 0x0000FFFFu : 0u) | (valid(tb) ? 0xFFFF0000u : 0u);
     mk23 = (valid(ta + 8) ? 0x0000FFFFu : 0u) | (valid(tb + 8) ? 0xFFFF0000u : 0u);
   }
