@@ -113,6 +113,17 @@ int prefetch_tiles(int cache_dtype) {
 
 namespace pa {
 int pdl_mode() { return g_pdl.load(std::memory_order_relaxed); }
+
+cudaError_t device_sm_count(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
+}
 }  // namespace pa
 
 extern "C" {
@@ -356,11 +367,8 @@ int decode_v1_impl(void* out, const void* q, int q_dtype, const void* k_cache,
 }
 
 int device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
-  return sms;
+  int sms = 0;
+  return pa::device_sm_count(&sms) == cudaSuccess ? sms : 148;
 }
 
 // Cascade workspace: the stacked partials (prefix splits + the suffix's), then the

@@ -6,9 +6,19 @@
 // fp32 scores (r = num_keep - num_recent): scores become unsigned keys of the same
 // order, and four passes of 8 bits count digits in shared memory and narrow the
 // threshold's digits, most significant first.  Tokens above the threshold stay, and of
-// those equal to it the first ones until r are found: whole-number counts, so the same
-// tokens every time.  A block scan over the tokens in their order gives each kept one
-// its place.
+// those equal to it the first ones until r are found; a token's place is the number of
+// tokens before it that are above the threshold plus that of equal ones, as far as they
+// stay.  Whole-number counts, so the same tokens every time.
+//
+// One cluster of 1 to 8 CTAs per (sequence, kv head), one launch: each CTA takes an equal
+// run of the tokens, its keys read once into shared memory, and the CTAs add up their
+// digit counts through distributed shared memory; then the cluster's threads copy the
+// kept rows, 16 bytes a thread, eight rows' loads before their stores.  Bound: the rows'
+// bytes once the selection (~8 us) is done.  (The first form, one CTA per (sequence, kv
+// head) and a second launch to move, spent 100 of its 144 us on the large case counting
+// digits on 64 of the SMs.)
+#include <cooperative_groups.h>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_tile.cuh"
@@ -16,7 +26,13 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeys = 4096;                    // keys a CTA holds; longer runs are read again
+constexpr int kMaxCluster = 8;
+constexpr int kMove = 8;                       // rows in flight per thread
 
 // Unsigned key with the order of the scores; NaN counts as lowest, -0 as 0.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -34,46 +50,73 @@ __device__ __forceinline__ int checked_len(const EvictArgs& a, int s) {
   return min(len, a.num_keep) > a.max_kept ? -1 : len;
 }
 
-__global__ void __launch_bounds__(kSelThreads)
-    evict_select_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, 4)
+    evict_kernel(const __grid_constant__ EvictArgs a) {
   constexpr uint32_t FULL = 0xffffffffu;
-  __shared__ uint32_t hist[256];
+  __shared__ __align__(8) uint32_t keys[kKeys];
+  __shared__ uint32_t hist[2][256];            // digit counts of this CTA, by pass parity
+  __shared__ uint32_t total[256];              // of the cluster
   __shared__ uint32_t pick[2];                 // digit, how many to take inside it
-  __shared__ uint32_t wsum[2][32];
-  const int kvh = blockIdx.x, s = blockIdx.y;
+  __shared__ uint32_t counts[2];               // this CTA's keys above / equal to the threshold
+  __shared__ uint32_t wcount[2][kWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = blockIdx.x, nc = gridDim.x, kvh = blockIdx.y, s = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
   griddep_wait();
   const int len = checked_len(a, s);
-  int* kept = a.kept + (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.kept_stride;
-  if (len < 0) {                               // skipped: nothing kept
-    if (tid == 0 && kvh == 0) {
+  const size_t unit = static_cast<size_t>(s) * a.num_kv_heads + kvh;
+  int* kept = a.kept + unit * a.kept_stride;
+  if (len < 0) {                               // skipped (the whole cluster): nothing kept
+    if (tid == 0 && kvh == 0 && rank == 0) {
       report_error(a.err_flag, kErrSeqLen);
       a.new_lens[s] = 0;
     }
-    for (int i = tid; i < a.kept_stride; i += kSelThreads) kept[i] = -1;
+    for (int i = rank * kThreads + tid; i < a.kept_stride; i += nc * kThreads) kept[i] = -1;
     return;
   }
-  const float* sc = a.scores + (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride;
+  const float* sc = a.scores + unit * a.score_stride;
+  float* nsc = a.new_scores ? a.new_scores + unit * a.new_score_stride : nullptr;
   const int m = min(len, a.num_keep);
   const int old = max(0, len - a.num_recent);  // tokens that compete by score
   const int r = m - (len - old);               // how many of them stay
-  uint32_t thr = 0, eq = 0;                    // key of the r-th largest, how many equal to it stay
+  auto put = [&](int place, int t) {
+    kept[place] = t;
+    if (nsc) nsc[place] = sc[t];
+  };
   if (r > 0 && r < old) {
-    uint32_t mask = 0, want = static_cast<uint32_t>(r);
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    // this CTA's run of tokens, in whole warps of 32 for each of its warps
+    const int per_warp = ((old + nc * kWarps - 1) / (nc * kWarps) + 31) / 32 * 32;
+    const int run = per_warp * kWarps;
+    const int t_lo = min(old, rank * run), t_hi = min(old, t_lo + run);
+    const bool held = run <= kKeys;
+    if (held)
+      for (int t = t_lo + tid; t < t_hi; t += kThreads) keys[t - t_lo] = score_key(sc[t]);
+    auto key = [&](int t) { return held ? keys[t - t_lo] : score_key(sc[t]); };
+    uint32_t thr = 0, mask = 0, want = static_cast<uint32_t>(r);
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass, buf = pass & 1;
+      if (tid < 256) hist[buf][tid] = 0;
       __syncthreads();
-      for (int t = tid; t < old; t += kSelThreads) {
-        const uint32_t k = score_key(sc[t]);
-        if ((k & mask) == thr) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      for (int t = t_lo + tid; t < t_hi; t += kThreads) {
+        const uint32_t k = key(t);
+        if ((k & mask) == thr) atomicAdd(&hist[buf][(k >> shift) & 255u], 1u);
+      }
+      cluster.sync();
+      if (tid < 256) {
+        uint32_t sum = 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < nc) sum += cluster.map_shared_rank(&hist[buf][0], c)[tid];
+        total[tid] = sum;
       }
       __syncthreads();
       if (warp == 0) {                         // lane l: digits 255 - 8l .. 248 - 8l
         uint32_t c[8], sum = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          c[i] = hist[255 - 8 * lane - i];
+          c[i] = total[255 - 8 * lane - i];
           sum += c[i];
         }
         uint32_t incl = sum;
@@ -98,91 +141,141 @@ __global__ void __launch_bounds__(kSelThreads)
       thr |= pick[0] << shift;
       want = pick[1];
       mask |= 255u << shift;
-      __syncthreads();
     }
-    eq = want;
+    // `want` of the tokens equal to the threshold stay, the first ones
+    const int w_lo = min(t_hi, t_lo + warp * per_warp), w_hi = min(t_hi, w_lo + per_warp);
+    uint32_t above = 0, equal = 0;
+    for (int t0 = w_lo; t0 < w_hi; t0 += 32) {
+      const uint32_t k = t0 + lane < w_hi ? key(t0 + lane) : 0u;
+      const bool in = t0 + lane < w_hi;
+      above += __popc(__ballot_sync(FULL, in && k > thr));
+      equal += __popc(__ballot_sync(FULL, in && k == thr));
+    }
+    if (lane == 0) {
+      wcount[0][warp] = above;
+      wcount[1][warp] = equal;
+    }
+    __syncthreads();
+    if (tid < 2) {
+      uint32_t sum = 0;
+      for (int w = 0; w < kWarps; ++w) sum += wcount[tid][w];
+      counts[tid] = sum;
+    }
+    cluster.sync();
+    above = equal = 0;                         // before this warp's first token
+    for (int c = 0; c < rank; ++c) {
+      const uint32_t* other = cluster.map_shared_rank(&counts[0], c);
+      above += other[0];
+      equal += other[1];
+    }
+    for (int w = 0; w < warp; ++w) {
+      above += wcount[0][w];
+      equal += wcount[1][w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (int t0 = w_lo; t0 < w_hi; t0 += 32) {
+      const int t = t0 + lane;
+      const uint32_t k = t < w_hi ? key(t) : 0u;
+      const uint32_t ba = __ballot_sync(FULL, t < w_hi && k > thr);
+      const uint32_t be = __ballot_sync(FULL, t < w_hi && k == thr);
+      const uint32_t eq_before = equal + __popc(be & below);
+      const uint32_t place = above + __popc(ba & below) + min(eq_before, want);
+      if (((ba >> lane) & 1u) || (((be >> lane) & 1u) && eq_before < want))
+        put(static_cast<int>(place), t);
+      above += __popc(ba);
+      equal += __popc(be);
+    }
+  } else if (r > 0) {                          // all of them stay
+    for (int t = rank * kThreads + tid; t < old; t += nc * kThreads) put(t, t);
   }
-  const bool all = r >= old, none = r <= 0;
+  for (int t = old + rank * kThreads + tid; t < len; t += nc * kThreads) put(r + t - old, t);
+  for (int i = m + rank * kThreads + tid; i < a.kept_stride; i += nc * kThreads) kept[i] = -1;
+  if (tid == 0 && kvh == 0 && rank == 0) a.new_lens[s] = m;
+  // every place is written (the barrier orders the cluster's global writes too), and
+  // nobody reads this CTA's shared memory any more
+  cluster.sync();
 
-  // ---- the kept ones in their order: chunks of one token per thread, two counts a
-  // chunk (equal to the threshold, kept)
-  uint32_t n_eq = 0, n_kept = 0;
-  for (int base = 0; base < len; base += kSelThreads) {
-    const int t = base + tid;
-    const uint32_t k = t < old ? score_key(sc[t]) : 0u;
-    const bool is_eq = !all && !none && t < old && k == thr;
-    const uint32_t be = __ballot_sync(FULL, is_eq);
-    if (lane == 0) wsum[0][warp] = __popc(be);
-    __syncthreads();
-    uint32_t rank = n_eq + __popc(be & ((1u << lane) - 1u)), tot = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) rank += wsum[0][w];
-      tot += wsum[0][w];
+  // ---- copy the kept rows: this CTA takes a run of places; their source and destination
+  // slots go to shared memory first (in place of the keys), so that a row's copy waits
+  // for one load, not for the place, the table and the row one after another
+  const int vshift = a.vec_shift;                          // 2 * row_vecs = 1 << vshift
+  const int bsh = a.block_shift, bmask = (1 << bsh) - 1;
+  const int v = tid & ((1 << vshift) - 1), rows = kThreads >> vshift;
+  const bool is_v = v >= a.row_vecs;
+  const size_t pitch = static_cast<size_t>(a.num_kv_heads) * a.row_vecs;
+  uint4* pool = static_cast<uint4*>(is_v ? a.v_cache : a.k_cache) +
+                static_cast<size_t>(kvh) * a.row_vecs + (is_v ? v - a.row_vecs : v);
+  const int32_t* stab = a.src_tables + static_cast<size_t>(s) * a.max_src_blocks;
+  const int32_t* dtab = a.dst_tables + static_cast<size_t>(s) * a.max_dst_blocks;
+  int2* moves = reinterpret_cast<int2*>(keys);             // (source, destination) slots
+  const int per = (m + nc - 1) / nc;
+  const int end = min(m, (rank + 1) * per);
+  for (int base = rank * per; base < end; base += kKeys / 2) {
+    const int n = min(end - base, kKeys / 2);
+    for (int i = tid; i < n; i += kThreads) {
+      const int j = base + i, t = __ldcg(kept + j);
+      const int sb = stab[t >> bsh], db = dtab[j >> bsh];
+      const bool ok = sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks;
+      const int from = (sb << bsh) + (t & bmask), to = (db << bsh) + (j & bmask);
+      if (!ok) report_error(a.err_flag, kErrBlockId);      // not copied
+      moves[i] = ok ? make_int2(from, to) : make_int2(-1, -1);
+      if (ok && a.k_scale) {
+        const size_t f = ((static_cast<size_t>(sb) * a.num_kv_heads + kvh) << bsh) + (t & bmask);
+        const size_t g = ((static_cast<size_t>(db) * a.num_kv_heads + kvh) << bsh) + (j & bmask);
+        a.k_scale[g] = a.k_scale[f];
+        a.v_scale[g] = a.v_scale[f];
+      }
     }
-    n_eq += tot;
-    const bool stay = t < len && (t >= old || all || (!none && (k > thr || (is_eq && rank < eq))));
-    const uint32_t bk = __ballot_sync(FULL, stay);
-    if (lane == 0) wsum[1][warp] = __popc(bk);
     __syncthreads();
-    uint32_t at = n_kept + __popc(bk & ((1u << lane) - 1u));
-    tot = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) at += wsum[1][w];
-      tot += wsum[1][w];
-    }
-    n_kept += tot;
-    if (stay) {
-      kept[at] = t;
-      if (a.new_scores)
-        a.new_scores[(static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.new_score_stride + at] = sc[t];
+    for (int i0 = tid >> vshift; i0 < n; i0 += kMove * rows) {
+      uint4 x[kMove];
+      int to[kMove];
+#pragma unroll
+      for (int u = 0; u < kMove; ++u) {
+        const int i = i0 + u * rows;
+        const int2 mv = i < n ? moves[i] : make_int2(-1, -1);
+        to[u] = mv.y;
+        if (mv.y >= 0) x[u] = pool[mv.x * pitch];
+      }
+#pragma unroll
+      for (int u = 0; u < kMove; ++u)
+        if (to[u] >= 0) pool[to[u] * pitch] = x[u];
     }
     __syncthreads();
-  }
-  for (int i = m + tid; i < a.kept_stride; i += kSelThreads) kept[i] = -1;
-  if (tid == 0 && kvh == 0) a.new_lens[s] = m;
-}
-
-// Move the kept rows: one warp per (place, kv head), a row's K and V by 16-byte vectors.
-__global__ void __launch_bounds__(256)
-    evict_move_kernel(const __grid_constant__ EvictArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int s = blockIdx.z, kvh = blockIdx.y;
-  const int j = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (j >= a.max_kept) return;
-  const int t = a.kept[(static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.kept_stride + j];
-  if (t < 0) return;
-  const int bs = a.block_size;
-  const int sb = a.src_tables[static_cast<size_t>(s) * a.max_src_blocks + t / bs];
-  const int db = a.dst_tables[static_cast<size_t>(s) * a.max_dst_blocks + j / bs];
-  if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
-    if (lane == 0) report_error(a.err_flag, kErrBlockId);
-    return;
-  }
-  const size_t src = ((static_cast<size_t>(sb) * bs + t % bs) * a.num_kv_heads + kvh) * a.row_vecs;
-  const size_t dst = ((static_cast<size_t>(db) * bs + j % bs) * a.num_kv_heads + kvh) * a.row_vecs;
-  for (int i = lane; i < 2 * a.row_vecs; i += 32) {
-    uint4* c = static_cast<uint4*>(i < a.row_vecs ? a.k_cache : a.v_cache);
-    const int v = i < a.row_vecs ? i : i - a.row_vecs;
-    c[dst + v] = c[src + v];
-  }
-  if (a.k_scale && lane < 2) {
-    float* sc = lane == 0 ? a.k_scale : a.v_scale;
-    sc[(static_cast<size_t>(db) * a.num_kv_heads + kvh) * bs + j % bs] =
-        sc[(static_cast<size_t>(sb) * a.num_kv_heads + kvh) * bs + t % bs];
   }
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
-  const bool pdl = pdl_mode() != 0;
-  cudaError_t e = launch_kernel(evict_select_kernel, dim3(a.num_kv_heads, a.num_seqs),
-                                dim3(kSelThreads), 0, stream, pdl, a);
+cudaError_t launch_evict(const EvictArgs& a0, cudaStream_t stream) {
+  EvictArgs a = a0;
+  a.vec_shift = 0;
+  while ((1 << a.vec_shift) < 2 * a.row_vecs) ++a.vec_shift;   // row_vecs and the block size
+  a.block_shift = 0;                                           // are powers of two
+  while ((1 << a.block_shift) < a.block_size) ++a.block_shift;
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  return launch_kernel(evict_move_kernel, dim3((a.max_kept + 7) / 8, a.num_kv_heads, a.num_seqs),
-                       dim3(256), 0, stream, pdl, a);
+  // CTAs per (sequence, kv head): until four fill an SM, while each has 256 tokens to look at
+  const long long cap = static_cast<long long>(a.max_src_blocks) * a.block_size;
+  const long long width = cap < a.score_stride ? cap : a.score_stride;
+  const long long units = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
+  unsigned nc = 1;
+  while (nc < kMaxCluster && units * nc < 4LL * sms && width >= 512LL * nc) nc *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(nc, a.num_kv_heads, a.num_seqs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = nc;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_mode() != 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_kernel, a);
 }
 
 }  // namespace pa

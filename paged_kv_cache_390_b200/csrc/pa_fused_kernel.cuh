@@ -31,6 +31,7 @@
 // for, the scores x and each row's log-sum-exp go to the workspace.
 #pragma once
 
+#include <atomic>
 #include <climits>
 
 #include "pa_device.cuh"
@@ -614,11 +615,20 @@ cudaError_t launch_fused_t(const FusedArgs& a0, size_t ws_bytes, cudaStream_t st
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0, per_sm = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kFusedWarps * 32, smem)) !=
-      cudaSuccess)
-    return e;
+  if ((e = device_sm_count(&sms)) != cudaSuccess) return e;
+  // the occupancy for this much shared memory, asked once per device and size (~2 us)
+  static std::atomic<long long> asked[2][64];
+  std::atomic<long long>& known = asked[cfg == &configured ? 0 : 1][dev & 63];
+  const long long k = known.load(std::memory_order_relaxed);
+  if (k != 0 && (k >> 16) == smem && dev < 64) {
+    per_sm = static_cast<int>(k & 0xffff);
+  } else {
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kFusedWarps * 32, smem)) !=
+        cudaSuccess)
+      return e;
+    if (dev < 64)
+      known.store((static_cast<long long>(smem) << 16) | per_sm, std::memory_order_relaxed);
+  }
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   if (per_sm > kFusedMaxCtasPerSm) per_sm = kFusedMaxCtasPerSm;
   if (a.ctas_per_sm > 0 && per_sm > a.ctas_per_sm) per_sm = a.ctas_per_sm;

@@ -68,6 +68,9 @@ struct DecodeArgs {
   const float* prior_l;       // [splits, S, H]
 };
 
+// SM count of the current device (asked once per device).
+cudaError_t device_sm_count(int* sms);
+
 // Current PDL mode (see pa_set_pdl).
 int pdl_mode();
 
@@ -140,6 +143,7 @@ struct EvictArgs {
   int max_kept;               // places every output has room for, at most num_keep
   int num_seqs, num_kv_heads, block_size, num_blocks;
   int row_vecs;               // 16-byte vectors per (token, kv head) row
+  int vec_shift, block_shift; // log2 of 2 * row_vecs and block_size, set by launch_evict
 };
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);

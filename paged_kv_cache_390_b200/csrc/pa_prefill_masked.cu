@@ -25,7 +25,8 @@ cudaError_t launch_mod(const PrefillArgs& a, int max_query_len, cudaStream_t str
   }
   if (e != cudaSuccess) return e;
   auto kern = prefill_kernel<QT, 0, MOD>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static int configured[64] = {0};
+  e = opt_in_smem(reinterpret_cast<const void*>(kern), kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   const int rows_per_cta = kQTiles * (kRows / G);
   const dim3 grid((max_query_len + rows_per_cta - 1) / rows_per_cta, a.num_kv_heads, a.num_seqs);

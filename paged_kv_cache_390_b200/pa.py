@@ -7,7 +7,6 @@ is no fallback: if the library is missing this module raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -125,37 +124,56 @@ def _stream(stream):
 
 def _same_device(*tensors) -> torch.device:
     """The CUDA device that all the tensors are on."""
-    dev = tensors[0].device
-    if dev.type != "cuda":
+    first = tensors[0]
+    if not first.is_cuda:
         raise ValueError("tensors passed to libpa must be CUDA tensors")
+    index = first.get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors of one call must be on one CUDA device")
-    return dev
+    return first.device
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
+class _on:
     """Make `dev` current, and `stream` (if given) torch's stream there, so that what the
-    call allocates belongs to the stream that uses it; yields the stream's handle."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream().cuda_stream
-    elif stream is None:
-        with torch.cuda.device(dev):
-            yield torch.cuda.current_stream().cuda_stream
-    else:
-        if stream.device != dev:
-            raise ValueError("the stream and the tensors must be on one CUDA device")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+    call allocates belongs to the stream that uses it; yields the stream's handle.  The
+    usual case (the current device and stream) costs one lookup of the handle."""
+    __slots__ = ("dev", "ctx")
+
+    def __init__(self, dev, stream):
+        self.dev = dev
+        self.ctx = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError("the stream and the tensors must be on one CUDA device")
+            self.ctx = torch.cuda.stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.dev.index)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            return self.ctx.__exit__(*exc)
 
 
-def _row_stride(t) -> int:
+def _addr(t):
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libpa must be contiguous")
+    return t.data_ptr()
+
+
+def _row_stride(t, T, heads, D) -> int:
     """Token stride of [T, heads, D] rows whose last two dimensions are dense."""
-    T, heads, D = t.shape
-    if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+    token, head, elem = t.stride()
+    if T and (elem != 1 or (heads > 1 and head != D)):
         raise ValueError("a token's rows must be dense")
-    return t.stride(0) if T > 1 else heads * D
+    return token if T > 1 else heads * D
 
 
 def _batch_checks(block_tables, seq_lens, num_seqs) -> None:
@@ -236,14 +254,14 @@ def rope_and_cache(q, key, value, positions, inv_freq, pair_axis, k_cache, v_cac
     value [T, H_kv, D] may be slices of a fused projection (rows dense, any token
     stride); out=q turns dense queries in place."""
     num_blocks, block_size, num_kv_heads, head_dim = k_cache.shape
-    num_tokens, num_heads, _ = q.shape
+    num_tokens, num_heads, q_dim = q.shape
     num_axes = positions.shape[0] if positions.dim() == 2 else 1
-    if (q.shape[2] != head_dim or key.shape != (num_tokens, num_kv_heads, head_dim)
-            or value.shape != key.shape or v_cache.shape != k_cache.shape
-            or positions.shape[-1] != num_tokens or slot_mapping.shape != (num_tokens,)
-            or pair_axis.shape != inv_freq.shape or inv_freq.dim() != 1):
+    rows, pairs, dtype = (num_tokens, num_kv_heads, head_dim), inv_freq.shape, q.dtype
+    if (q_dim != head_dim or key.shape != rows or value.shape != rows
+            or positions.shape[-1] != num_tokens or positions.dim() > 2
+            or slot_mapping.shape != (num_tokens,) or pair_axis.shape != pairs or len(pairs) != 1):
         raise ValueError("shapes of q, key, value, positions, slots, frequencies and caches differ")
-    if key.dtype != q.dtype or value.dtype != q.dtype:
+    if key.dtype != dtype or value.dtype != dtype:
         raise ValueError("key and value must have q's dtype")
     if (positions.dtype != torch.int64 or slot_mapping.dtype != torch.int64
             or inv_freq.dtype != torch.float64 or pair_axis.dtype != torch.int32):
@@ -253,15 +271,17 @@ def rope_and_cache(q, key, value, positions, inv_freq, pair_axis, k_cache, v_cac
                        slot_mapping, k_scale, v_scale, err_flag, out)
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty((num_tokens, num_heads, head_dim), dtype=q.dtype, device=dev)
-        elif out.shape != q.shape or out.dtype != q.dtype:
+            out = torch.empty((num_tokens, num_heads, head_dim), dtype=dtype, device=dev)
+        elif out.shape != q.shape or out.dtype != dtype:
             raise ValueError("out must have q's shape and dtype")
         rc = lib().pa_rope_and_cache(
-            _ptr(out), q.data_ptr(), key.data_ptr(), value.data_ptr(), _FLOAT_CODES[q.dtype],
-            _row_stride(q), _row_stride(key), _row_stride(value), _ptr(positions), num_axes,
-            _ptr(inv_freq), _ptr(pair_axis), 2 * inv_freq.shape[0], int(bool(interleaved)),
-            _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
-            num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, _ptr(err_flag),
+            _addr(out), q.data_ptr(), key.data_ptr(), value.data_ptr(), _FLOAT_CODES[dtype],
+            _row_stride(q, num_tokens, num_heads, head_dim),
+            _row_stride(key, num_tokens, num_kv_heads, head_dim),
+            _row_stride(value, num_tokens, num_kv_heads, head_dim), _addr(positions), num_axes,
+            _addr(inv_freq), _addr(pair_axis), 2 * pairs[0], int(bool(interleaved)),
+            _addr(k_cache), _addr(v_cache), code, _addr(k_scale), _addr(v_scale), _addr(slot_mapping),
+            num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, _addr(err_flag),
             s)
     _check(rc, "pa_rope_and_cache")
     return out
@@ -352,12 +372,12 @@ def decode_masked(q, k_cache, v_cache, block_tables, seq_lens, scale, *, softcap
         if out is None:
             out = torch.empty_like(q)
         rc = lib().pa_decode_masked(
-            _ptr(out), _ptr(q), _FLOAT_CODES[q.dtype], _ptr(k_cache), _ptr(v_cache), code,
-            _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
-            _ptr(seq_lens), num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
-            float(scale), float(softcap), _ptr(alibi_slopes), _ptr(kv_start), int(window),
-            _ptr(scores_in), _ptr(scores_out), width, _ptr(workspace.buf), workspace.nbytes,
-            _ptr(err_flag), s)
+            _addr(out), _addr(q), _FLOAT_CODES[q.dtype], _addr(k_cache), _addr(v_cache), code,
+            _addr(k_scale), _addr(v_scale), _addr(block_tables), block_tables.shape[1],
+            _addr(seq_lens), num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
+            float(scale), float(softcap), _addr(alibi_slopes), _addr(kv_start), int(window),
+            _addr(scores_in), _addr(scores_out), width, _addr(workspace.buf), workspace.nbytes,
+            _addr(err_flag), s)
     _check(rc, "pa_decode_masked")
     return out
 
@@ -389,11 +409,11 @@ def prefill_masked(q, k_cache, v_cache, block_tables, seq_lens, query_start, sca
         if out is None:
             out = torch.empty_like(q)
         rc = lib().pa_prefill_masked(
-            _ptr(out), _ptr(q), _FLOAT_CODES[q.dtype], _ptr(query_start), total_q,
-            int(max_query_len), _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), num_seqs, num_heads,
+            _addr(out), _addr(q), _FLOAT_CODES[q.dtype], _addr(query_start), total_q,
+            int(max_query_len), _addr(k_cache), _addr(v_cache), code, _addr(k_scale), _addr(v_scale),
+            _addr(block_tables), block_tables.shape[1], _addr(seq_lens), num_seqs, num_heads,
             num_kv_heads, head_dim, block_size, num_blocks, float(scale), float(softcap),
-            _ptr(alibi_slopes), _ptr(kv_start), _ptr(prefix_lens), int(window), _ptr(err_flag), s)
+            _addr(alibi_slopes), _addr(kv_start), _addr(prefix_lens), int(window), _addr(err_flag), s)
     _check(rc, "pa_prefill_masked")
     return out
 
@@ -429,12 +449,12 @@ def evict(k_cache, v_cache, block_tables, seq_lens, new_block_tables, scores, nu
         if new_lens.dtype != torch.int32 or new_lens.shape != (num_seqs,):
             raise ValueError("new_lens must be int32 [num_seqs]")
         rc = lib().pa_evict(
-            _ptr(k_cache), _ptr(v_cache), code, _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
-            block_tables.shape[1], _ptr(seq_lens), _ptr(new_block_tables),
-            new_block_tables.shape[1], _ptr(scores), scores.shape[2], int(num_keep),
-            int(num_recent), _ptr(kept), kept.shape[2], _ptr(new_scores), new_scores.shape[2],
-            _ptr(new_lens), num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
-            _ptr(err_flag), s)
+            _addr(k_cache), _addr(v_cache), code, _addr(k_scale), _addr(v_scale), _addr(block_tables),
+            block_tables.shape[1], _addr(seq_lens), _addr(new_block_tables),
+            new_block_tables.shape[1], _addr(scores), scores.shape[2], int(num_keep),
+            int(num_recent), _addr(kept), kept.shape[2], _addr(new_scores), new_scores.shape[2],
+            _addr(new_lens), num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
+            _addr(err_flag), s)
     _check(rc, "pa_evict")
     return kept, new_lens, new_scores
 
