@@ -66,6 +66,16 @@ struct DecodeArgs {
   const float* prior_o;       // [splits, S, H, D] or null
   const float* prior_m;       // [splits, S, H]
   const float* prior_l;       // [splits, S, H]
+  // Changed scores (pa_decode_masked; the MASK build only).
+  const float* slopes;        // [H] or null
+  const int32_t* kv_start;    // [S] or null
+  float cap_in;               // scale / softcap (0: no cap)
+  float cap_log2;             // softcap * log2(e)
+  int window;                 // 0: no limit
+  const float* scores_in;     // [S, H_kv, score_stride] or null
+  float* scores_out;          // or null: no running scores
+  float* logits;              // workspace [S, H_kv, score_stride, G], log2 units
+  int score_stride;
 };
 
 // SM count of the current device (asked once per device).

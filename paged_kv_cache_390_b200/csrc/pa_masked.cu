@@ -8,6 +8,7 @@
 // its kv head, to a running score: the attention leaves its scores x in the workspace
 // and log-sum-exps beside them, and a second launch turns them into weights, so K is not
 // read twice.
+#include "pa_decode_kernel.cuh"
 #include "pa_fused_kernel.cuh"
 #include "pa_write.cuh"
 
@@ -131,28 +132,29 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// scores_out[s, kvh, t] = scores_in + sum over the group of 2^(x - lse): one thread per
-// (token, kv head, sequence).
+// scores_out[s, kvh, t] = scores_in + the weights of t under the kv head's query heads: one
+// thread per (token, kv head, sequence), for the forms that split a sequence over CTAs.
 __global__ void __launch_bounds__(256)
     masked_scores_kernel(const __grid_constant__ MaskedArgs a) {
+  __shared__ float lse[kMaxGroup];
   griddep_launch_dependents();
   griddep_wait();
-  const int t = blockIdx.x * 256 + threadIdx.x, kvh = blockIdx.y, s = blockIdx.z;
-  int len = a.seq_lens[s];
+  const int kvh = blockIdx.y, s = blockIdx.z;
+  const int len = a.seq_lens[s];
   if (len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_blocks) * a.block_size)
     return;                                       // a skipped sequence keeps its scores
-  if (t >= min(len, a.score_stride)) return;
+  const int n = min(len, a.score_stride);
+  if (blockIdx.x * 256 >= n) return;
   const int G = a.num_heads / a.num_kv_heads;
+  if (threadIdx.x < G)
+    lse[threadIdx.x] = a.lse[static_cast<size_t>(s) * a.num_heads + kvh * G + threadIdx.x];
+  __syncthreads();
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= n) return;
   const Span sp = seen_span(a.kv_start ? a.kv_start[s] : 0, len - 1, a.window, 0, len);
   const size_t i = (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride + t;
-  float w = 0.f;
-  if (t >= sp.lo && t < sp.hi) {
-    for (int g = 0; g < G; ++g) {
-      const float lse = a.lse[static_cast<size_t>(s) * a.num_heads + kvh * G + g];
-      if (lse != -INFINITY) w += exp2f(a.logits[i * G + g] - lse);
-    }
-  }
-  a.scores_out[i] = (a.scores_in ? a.scores_in[i] : 0.f) + w;
+  const float before = a.scores_in ? a.scores_in[i] : 0.f;
+  a.scores_out[i] = before + (t >= sp.lo ? token_weight(a.logits + i * G, lse, G) : 0.f);
 }
 
 template <typename QT, typename KT>
@@ -186,9 +188,12 @@ cudaError_t launch_attention(const MaskedArgs& a, int q_dtype, int cache_dtype, 
 namespace {
 
 template <typename QT, int KIND>
-cudaError_t masked_shape(const FusedArgs& a, int D, int BS, size_t ws, cudaStream_t s) {
+cudaError_t masked_shape(const FusedArgs& a, int D, int BS, size_t ws, cudaStream_t s,
+                         const DecodeArgs* v1, const DecodeShape& sh) {
 #define PA_CASE(DD, BB) \
-  if (D == DD && BS == BB) return launch_fused_t<QT, KIND, DD, BB, true>(a, ws, s);
+  if (D == DD && BS == BB)                                                             \
+    return v1 ? launch_tc<QT, KIND, DD, BB, true>(*v1, sh, s)                          \
+              : launch_fused_t<QT, KIND, DD, BB, true>(a, ws, s);
   PA_CASE(128, 16)
   PA_CASE(128, 8)
   PA_CASE(128, 32)
@@ -199,20 +204,38 @@ cudaError_t masked_shape(const FusedArgs& a, int D, int BS, size_t ws, cudaStrea
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_masked_fused(const FusedArgs& a, int q_dtype, int cache_dtype, int D, int BS,
-                                size_t ws, cudaStream_t s) {
+// The persistent form, or with v1 the one-CTA-per-(sequence, kv head) form.
+cudaError_t launch_masked_tc(const FusedArgs& a, int q_dtype, int cache_dtype, int D, int BS,
+                             size_t ws, cudaStream_t s, const DecodeArgs* v1,
+                             const DecodeShape& sh) {
   const bool qh = q_dtype == PA_F16;
   switch (cache_dtype) {
-    case PA_F16: return masked_shape<__half, kKind16>(a, D, BS, ws, s);
-    case PA_BF16: return masked_shape<__nv_bfloat16, kKind16>(a, D, BS, ws, s);
+    case PA_F16: return masked_shape<__half, kKind16>(a, D, BS, ws, s, v1, sh);
+    case PA_BF16: return masked_shape<__nv_bfloat16, kKind16>(a, D, BS, ws, s, v1, sh);
     case PA_INT8:
-      return qh ? masked_shape<__half, kKindI8>(a, D, BS, ws, s)
-                : masked_shape<__nv_bfloat16, kKindI8>(a, D, BS, ws, s);
+      return qh ? masked_shape<__half, kKindI8>(a, D, BS, ws, s, v1, sh)
+                : masked_shape<__nv_bfloat16, kKindI8>(a, D, BS, ws, s, v1, sh);
     case PA_FP8E4M3:
-      return qh ? masked_shape<__half, kKindE4M3>(a, D, BS, ws, s)
-                : masked_shape<__nv_bfloat16, kKindE4M3>(a, D, BS, ws, s);
+      return qh ? masked_shape<__half, kKindE4M3>(a, D, BS, ws, s, v1, sh)
+                : masked_shape<__nv_bfloat16, kKindE4M3>(a, D, BS, ws, s, v1, sh);
   }
   return cudaErrorInvalidValue;
+}
+
+// Warps per CTA of the one-CTA form, as pa_decode_v1 chooses them.
+int masked_warps(int cache_dtype) {
+  return cache_dtype == PA_INT8 || cache_dtype == PA_FP8E4M3 ? kMaxWarps : kDefaultWarps;
+}
+
+// One CTA per (sequence, kv head) where that fills the GPU with short ones, or where
+// there is little to split; else the persistent form, which spreads long or few ones over
+// every SM.
+bool pick_one_cta(const MaskedArgs& a, int cache_dtype, int num_sms) {
+  long long most = static_cast<long long>(a.max_blocks) * a.block_size;   // tokens a row sees
+  if (a.window > 0 && a.window + 15LL < most) most = a.window + 15LL;
+  const long long tiles = (most + 15) / 16;
+  const long long units = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
+  return (units >= num_sms && tiles <= 256) || tiles <= 4 * masked_warps(cache_dtype);
 }
 
 size_t lse_bytes(int num_seqs, int num_heads) {
@@ -270,8 +293,45 @@ cudaError_t launch_decode_masked(const MaskedArgs& a0, int q_dtype, int cache_dt
     f.lse = a.lse;
     f.logits = a.logits;
     f.score_stride = a.score_stride;
-    e = launch_masked_fused(f, q_dtype, cache_dtype, head_dim, a.block_size,
-                            fused_workspace_bytes(a.num_seqs, a.num_kv_heads, head_dim, num_sms), s);
+    DecodeShape sh{};
+    const bool one_cta = pick_one_cta(a, cache_dtype, num_sms);
+    DecodeArgs d{};
+    if (one_cta) {
+      sh.warps = masked_warps(cache_dtype);
+      sh.grid_x = 1;
+      d.out = a.out;
+      d.q = a.q;
+      d.k_cache = a.k_cache;
+      d.v_cache = a.v_cache;
+      d.k_scale = a.k_scale;
+      d.v_scale = a.v_scale;
+      d.block_tables = a.block_tables;
+      d.seq_lens = a.seq_lens;
+      d.err_flag = a.err_flag;
+      d.max_blocks = a.max_blocks;
+      d.num_seqs = a.num_seqs;
+      d.num_heads = a.num_heads;
+      d.num_kv_heads = a.num_kv_heads;
+      d.num_blocks = a.num_blocks;
+      d.stages = default_stages(cache_dtype, head_dim, a.block_size, sh.warps, 96);
+      d.scale_log2 = f.scale_log2;
+      d.timeout_ns = a.timeout_ns;
+      d.inject = a.inject;
+      d.pdl = f.pdl;
+      d.slopes = a.slopes;
+      d.kv_start = a.kv_start;
+      d.cap_in = f.cap_in;
+      d.cap_log2 = f.cap_log2;
+      d.window = a.window;
+      d.scores_in = a.scores_in;
+      d.scores_out = a.scores_out;
+      d.logits = a.logits;
+      d.score_stride = a.score_stride;
+    }
+    e = launch_masked_tc(f, q_dtype, cache_dtype, head_dim, a.block_size,
+                         fused_workspace_bytes(a.num_seqs, a.num_kv_heads, head_dim, num_sms), s,
+                         one_cta ? &d : nullptr, sh);
+    if (one_cta) return e;                   // its CTAs add the running scores themselves
   }
   if (e != cudaSuccess || !a.scores_out) return e;
   const long long cap = static_cast<long long>(a.max_blocks) * a.block_size;

@@ -44,4 +44,22 @@ __device__ __forceinline__ float tanh_f32(float y) {
   return a < 0.625f ? fmaf(y * z, q, y) : big;
 }
 
+// A cached token's weight summed over the G query heads of its kv head, from their scores
+// x and log-sum-exps (log2 units; -inf: that head's row saw nothing).
+__device__ __forceinline__ float token_weight(const float* x, const float* lse, int G) {
+  float w = 0.f;
+  if ((G & 3) == 0) {
+    for (int g = 0; g < G; g += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(x + g);
+      w += (lse[g] != -INFINITY ? exp2f(v.x - lse[g]) : 0.f) +
+           (lse[g + 1] != -INFINITY ? exp2f(v.y - lse[g + 1]) : 0.f) +
+           (lse[g + 2] != -INFINITY ? exp2f(v.z - lse[g + 2]) : 0.f) +
+           (lse[g + 3] != -INFINITY ? exp2f(v.w - lse[g + 3]) : 0.f);
+    }
+  } else {
+    for (int g = 0; g < G; ++g) w += lse[g] != -INFINITY ? exp2f(x[g] - lse[g]) : 0.f;
+  }
+  return w;
+}
+
 }  // namespace pa

@@ -166,13 +166,17 @@ def test_decode(pa, dt, cd, form):
 @pytest.mark.gpu
 @pytest.mark.parametrize("bs", [8, 16, 32])
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
 @pytest.mark.parametrize("dt,cd", PAIRS)
-def test_decode_documents_and_scores(pa, dt, cd, D, bs):
+def test_decode_documents_and_scores(pa, dt, cd, D, bs, wide):
     """Document starts everywhere in a tile and past the end (a row that sees nothing), with
-    running scores; scores past each length stay as they are."""
+    running scores; scores past each length stay as they are.  A wide table (the most
+    tokens a sequence could have) takes the persistent form."""
     lens = [1, 16, 40, 64, 100, 129, 300, 50, 31]
     starts = [0, 15, 17, 16, -4, 127, 250, 50, 90]
     b = Batch(dt, cd, lens, [1] * len(lens), 12, 4, D, bs, D + bs, softcap=20.0, starts=starts)
+    if wide:
+        b.table = torch.nn.functional.pad(b.table, (0, 1024 // bs), value=-1)
     width = 310
     g = torch.Generator().manual_seed(3)
     before = torch.rand((len(lens), 4, width), generator=g)
