@@ -14,7 +14,7 @@
 //   warp 8      TMA: Q once, then 128-token K and V tiles (one box per block
 //               and 64-column half) into rings of 3 (K) and 2 (V) stages, K
 //               running one tile ahead of V;
-//   warp 9      MMA: one thread issues every tcgen05.mma --
+//   warp 9      MMA: one elected lane issues every tcgen05.mma --
 //               S_x = Q_x K^T (M 128, N 128, K = head_dim; both operands in
 //               shared memory) into TMEM, and O_x += P_x V (N = head_dim, P
 //               read from TMEM, V MN-major from the TMA tile), in the order
@@ -410,10 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     const uint32_t idesc_s = umma_idesc_f16(kBf16, false, kRows, kBN);
     const uint32_t idesc_o = umma_idesc_f16(kBf16, true, kRows, kD);
-    auto wait1 = [&](int b, uint32_t parity) {
-      bool ok = true;
-      if (lane == 0) ok = mbar_wait_abortable(bar(b), parity, a.timeout_ns, abort);
-      return __shfl_sync(FULL, ok, 0) != 0;
+    auto wait1 = [&](int b, uint32_t parity) {   // the vote keeps the control flow uniform
+      return __all_sync(FULL, mbar_wait_abortable(bar(b), parity, a.timeout_ns, abort)) != 0;
     };
     // operand descriptors of the first stage / tile; a K slice, stage or tile
     // moves only the start-address field (bytes >> 4), which no offset here
@@ -422,35 +420,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dk0 = umma_desc_sw128(k_s(0), 16, 1024);
     const uint64_t dv0 = umma_desc_sw128(v_s(0), kKvHalf, 1024);
     auto issue_s = [&](int x, int j) {       // S_x = Q_x K_j^T
-      if (lane == 0) {
-        tc_fence_after_sync();
-        const uint64_t qd = dq0 + static_cast<uint64_t>(x * (2 * kQHalf >> 4));
-        const uint64_t kd = dk0 + static_cast<uint64_t>((j % kKst) * (kKvTile >> 4));
+      tc_fence_after_sync();
+      const uint64_t qd = dq0 + static_cast<uint64_t>(x * (2 * kQHalf >> 4));
+      const uint64_t kd = dk0 + static_cast<uint64_t>((j % kKst) * (kKvTile >> 4));
 #pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk) {
-          const uint32_t qoff = static_cast<uint32_t>(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4);
-          const uint32_t koff = static_cast<uint32_t>(((kk >> 2) * kKvHalf + (kk & 3) * 32) >> 4);
-          umma_f16_ss(t_s(x), qd + qoff, kd + koff, idesc_s, kk > 0);
-        }
-        umma_commit(bar(kBarSFull + x));
+      for (int kk = 0; kk < kD / 16; ++kk) {
+        const uint32_t qoff = static_cast<uint32_t>(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4);
+        const uint32_t koff = static_cast<uint32_t>(((kk >> 2) * kKvHalf + (kk & 3) * 32) >> 4);
+        umma_f16_ss_warp(t_s(x), qd + qoff, kd + koff, idesc_s, kk > 0);
       }
-      __syncwarp();
+      umma_commit_warp(bar(kBarSFull + x));
     };
     auto issue_pv = [&](int x, int j) {      // O_x += P_x V_j, P from TMEM
-      if (lane == 0) {
-        tc_fence_after_sync();
-        const uint64_t vd = dv0 + static_cast<uint64_t>((j % kVst) * (kKvTile >> 4));
+      tc_fence_after_sync();
+      const uint64_t vd = dv0 + static_cast<uint64_t>((j % kVst) * (kKvTile >> 4));
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
+      for (int part = 0; part < PARTS; ++part) {
 #pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk)
-            umma_f16_ts(t_o(x), t_s(x) + static_cast<uint32_t>(part * 64 + kk * 8),
-                        vd + static_cast<uint32_t>(kk * 16 * 128 >> 4), idesc_o,
-                        j > 0 || part > 0 || kk > 0);
-        }
-        umma_commit(bar(kBarODone + x));
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          umma_f16_ts_warp(t_o(x), t_s(x) + static_cast<uint32_t>(part * 64 + kk * 8),
+                           vd + static_cast<uint32_t>(kk * 16 * 128 >> 4), idesc_o,
+                           j > 0 || part > 0 || kk > 0);
       }
-      __syncwarp();
+      umma_commit_warp(bar(kBarODone + x));
     };
     bool ok = wait1(kBarQ, 0);
     if (ok && ntiles > 0) {
@@ -458,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         issue_s(0, 0);
         issue_s(1, 0);
-        if (lane == 0) umma_commit(bar(kBarKEmpty));       // K(0) is read by now
+        umma_commit_warp(bar(kBarKEmpty));                  // K(0) is read by now
       }
     }
     for (int j = 0; ok && j < ntiles; ++j) {
@@ -497,11 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!(ok = wait1(kBarPFull + 1, j & 1))) break;
       issue_pv(1, j);
-      if (lane == 0) umma_commit(bar(kBarVEmpty + vs));     // V(j) is read by now
+      umma_commit_warp(bar(kBarVEmpty + vs));               // V(j) is read by now
       if (j + 1 < ntiles) {
         if (!(ok = wait1(kBarODone + 1, j & 1))) break;   // P_B(j) consumed
         issue_s(1, j + 1);
-        if (lane == 0) umma_commit(bar(kBarKEmpty + (j + 1) % kKst));   // K(j+1) read
+        umma_commit_warp(bar(kBarKEmpty + (j + 1) % kKst));  // K(j+1) read
       }
     }
   } else {
@@ -659,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();                           // every role is done issuing and waiting
-  if (*abort && lane == 0) {
+  if (*abort && (lane == 0 || warp == kMmaWarp)) {
     if (warp == kTmaWarp) {                  // let the copies in flight land
       for (int st = 0; st < kKst; ++st)
         if (armed_k[st] >= 0)
@@ -668,8 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (armed_v[st] >= 0)
           mbar_wait_bounded(bar(kBarVFull + st), (armed_v[st] / kVst) & 1, kDrainLimitNs);
     } else if (warp == kMmaWarp) {           // let the MMAs in flight finish
-      report_error(a.err_flag, kErrTimeout);
-      umma_commit(bar(kBarDrain));
+      if (lane == 0) report_error(a.err_flag, kErrTimeout);
+      __syncwarp();
+      umma_commit_warp(bar(kBarDrain));
       mbar_wait_bounded(bar(kBarDrain), 0, kDrainLimitNs);
     }
   }
