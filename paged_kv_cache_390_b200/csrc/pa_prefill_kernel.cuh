@@ -89,8 +89,11 @@ constexpr int kKOff = kQTiles * 2 * kQHalf;
 constexpr int kVOff = kKOff + kKst * kKvTile;
 constexpr int kSmemBytes = kVOff + kVst * kKvTile + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;        // S_A, S_B, O_A, O_B: 128 columns each
-constexpr int kThreads = 320;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+// Softmax warps: one thread per row (8 warps), or two with MOD >= 0 (16 warps).
+template <int MOD>
+__host__ __device__ constexpr int softmax_warps() { return MOD >= 0 ? 16 : 8; }
+template <int MOD>
+__host__ __device__ constexpr int prefill_threads() { return 32 * (softmax_warps<MOD>() + 2); }
 
 // bf16 keeps 8 significant bits: P goes in as a high and a low bf16 part (two
 // PV products, ~16 bits); fp16's 11 bits need one.  P of 128 tokens takes 64
@@ -98,6 +101,12 @@ constexpr int kTmaWarp = 8, kMmaWarp = 9;
 template <typename QT, int MOD>
 __host__ __device__ constexpr int p_parts() {
   return MOD >= 0 || std::is_same<QT, __nv_bfloat16>::value ? 2 : 1;
+}
+
+// MOD >= 0: TMEM column (from S) of the P operand of tokens [16 kk, 16 kk + 16): the
+// 32-column chunk of 32 tokens holds 16 columns of high parts, then 16 of low parts.
+__device__ __forceinline__ uint32_t mask_p_col(int part, int kk) {
+  return static_cast<uint32_t>((kk >> 1) * 32 + part * 16 + (kk & 1) * 8);
 }
 
 // ---- packed f32x2 arithmetic: two FP32 results per instruction
@@ -136,7 +145,9 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 enum {
   kBarQ = 0, kBarKFull = 1, kBarKEmpty = kBarKFull + kKst, kBarVFull = kBarKEmpty + kKst,
   kBarVEmpty = kBarVFull + kVst, kBarSFull = kBarVEmpty + kVst, kBarPFull = kBarSFull + 2,
-  kBarODone = kBarPFull + 2, kBarDrain = kBarODone + 2, kNumBars
+  kBarODone = kBarPFull + 2, kBarDrain = kBarODone + 2,
+  kBarPair = kBarDrain + 1,                  // MOD >= 0: a row's two threads (8 warp pairs)
+  kNumBars = kBarPair + 8
 };
 
 // MOD >= 0: y -> factor * tanh(y) for |y| <= 1, as factor * y * Q(y^2): Q of degree 5
@@ -212,7 +223,7 @@ __device__ __noinline__ void masked_row(const PrefillArgs& a, const int32_t* tab
 
 // BSC: tokens per block, 0: a.block_size.
 template <typename QT, int BSC, int MOD = -1>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PrefillArgs a) {
   constexpr bool MASK = MOD >= 0, CAP = MASK && (MOD & 1), BIAS = MASK && (MOD & 2);
@@ -221,12 +232,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int NBOX = kBN / BOXH;             // boxes per 64-column half
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
   constexpr int PARTS = p_parts<QT, MOD>();
+  constexpr int NSM = softmax_warps<MOD>();
+  constexpr int TW = NSM / 2;                // softmax warps per query tile
+  constexpr int HALVES = TW / 4;             // threads per row
+  constexpr int kTmaWarp = NSM, kMmaWarp = NSM + 1;
   constexpr uint32_t FULL = 0xffffffffu;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
-  __shared__ int span_lo[8], span_hi[8];     // MASK: the union of each softmax warp's spans
+  __shared__ int span_lo[NSM], span_hi[NSM];  // MASK: the union of each softmax warp's spans
+  // MASK: each softmax thread's maximum for the row's other thread (whole log2 units;
+  // kNone: no seen token).  One buffer: a thread writes step j + 1's only after S(j + 1),
+  // so after both threads of the row have handed over P(j), having read step j's.
+  constexpr int kNone = -32768;
+  __shared__ int16_t pair_max[MASK ? 512 : 1];
 
   const int tile2 = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -258,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // MASK: this thread's row and the tokens it sees; the union of the CTA's rows
   int row_lo = 0, row_hi = 0, row_pos = -1, u_lo = 0, u_hi = 0;
   if constexpr (MASK) {
-    if (warp < 8) {
-      const int r = (tid % kRows) / G, tok = row0 + (warp / 4) * TQ + r;
+    if (warp < NSM) {
+      const int r = (tid % kRows) / G, tok = row0 + (warp / TW) * TQ + r;
       if (r < TQ && tok < q_len) {
         row_pos = L - q_len + tok;
         const Span sp = seen_span(a.kv_start ? a.kv_start[q0 + tok] : 0, row_pos, a.window,
@@ -295,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const bool from_threads = i >= kBarPFull && i < kBarPFull + 2;
-      mbar_init(bar(i), from_threads ? kRows : 1);
+      mbar_init(bar(i), from_threads ? kRows * HALVES : (i >= kBarPair ? 64 : 1));
     }
     abort_flag = 0;
     fence_barrier_init();
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (MASK) {
     u_lo = span_lo[0];
     u_hi = span_hi[0];
-    for (int w = 1; w < 8; ++w) {
+    for (int w = 1; w < NSM; ++w) {
       u_lo = min(u_lo, span_lo[w]);
       u_hi = max(u_hi, span_hi[w]);
     }
@@ -326,12 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto t_s = [&](int x) { return tmem + static_cast<uint32_t>(128 * x); };
   auto t_o = [&](int x) { return tmem + 256u + static_cast<uint32_t>(128 * x); };
 
-  // softmax state (warps 0-7), kept here for the epilogue
-  const int x_me = warp < 8 ? warp / 4 : 0;
+  // softmax state, kept here for the epilogue
+  const int x_me = warp < NSM ? warp / TW : 0;
+  const int half_me = MASK && warp < NSM ? (warp / 4) % HALVES : 0;
   const int row_me = tid % kRows;
   const int r_tok = row_me / G;
   const int tok_me = row0 + x_me * TQ + r_tok;          // query token within the chunk
-  const bool row_valid = warp < 8 && tok_me < q_len && (!MASK || r_tok < TQ);
+  const bool row_valid = warp < NSM && tok_me < q_len && (!MASK || r_tok < TQ);
   float m_run = -INFINITY, l_run = 0.f;
   int armed_k[kKst], armed_v[kVst];          // TMA warp: last tile issued into each stage
 #pragma unroll
@@ -438,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int part = 0; part < PARTS; ++part) {
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_f16_ts_warp(t_o(x), t_s(x) + static_cast<uint32_t>(part * 64 + kk * 8),
+          umma_f16_ts_warp(t_o(x), t_s(x) + (MASK ? mask_p_col(part, kk)
+                                                  : static_cast<uint32_t>(part * 64 + kk * 8)),
                            vd + static_cast<uint32_t>(kk * 16 * 128 >> 4), idesc_o,
                            j > 0 || part > 0 || kk > 0);
       }
@@ -503,147 +525,237 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = !row_valid ? -1 : (cascade ? L - 1 : L - q_len + tok_me);
     float slope = 0.f;
     if (BIAS && row_valid) slope = a.slopes[kvh * G + row_me % G] * kLog2e;
-    for (int j = 0; j < ntiles; ++j) {
-      // S_x(j) complete also means PV_x(j-1) is: its MMA waited for that
-      if (!mbar_wait_abortable(bar(kBarSFull + x), j & 1, a.timeout_ns, abort)) break;
-      tc_fence_after_sync();
-      float sv[kBN];
+    if constexpr (MASK) {
+      // Two threads per row, columns [64 half, 64 half + 64): scores in registers, the
+      // row's maximum exchanged, P over the columns each thread has read (a 32-column
+      // chunk holds its tokens' 16 columns of high parts, then 16 of low parts).
+      constexpr int NC = kBN / HALVES;       // columns per thread
+      const int pair = x * 4 + (warp & 3);
+      const int mine = (x * 2 + half_me) * kRows + row_me, other = (x * 2 + 1 - half_me) * kRows + row_me;
+      const uint32_t s_col = t_s(x) + lane_off + static_cast<uint32_t>(half_me * NC);
+      for (int j = 0; j < ntiles; ++j) {
+        if (!mbar_wait_abortable(bar(kBarSFull + x), j & 1, a.timeout_ns, abort)) break;
+        tc_fence_after_sync();
+        float sv[NC];
 #pragma unroll
-      for (int i = 0; i < kBN / 32; ++i) {
-        float v[32];
-        tmem_ld32(t_s(x) + lane_off + 32 * i, v);
+        for (int i = 0; i < NC / 32; ++i) {
+          float v[32];
+          tmem_ld32(s_col + 32 * i, v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sv[32 * i + e] = v[e];
-      }
-      tmem_wait_ld();
-
-      // the row max of scale * s (log2 units), taken on the raw dot products:
-      // the largest for scale >= 0, the smallest otherwise; four independent
-      // chains; no per-element mask on a tile that lies wholly inside this
-      // row's causal window
-      const int t_base = (t_lo + j) * kBN;
-      const bool full = MASK ? row_lo <= t_base && row_hi >= t_base + kBN : t_base + kBN - 1 <= pos;
-      const int nvalid = full ? kBN : max(0, MASK ? row_hi - t_base : pos - t_base + 1);
-      const int nskip = MASK ? row_lo - t_base : 0;        // columns [nskip, nvalid) are seen
-      float factor = a.scale_log2;           // what turns sv into scores in log2 units
-      if constexpr (CAP) {
-        float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < kBN; c += 2)
-          big[(c >> 1) & 3] = fmax3(big[(c >> 1) & 3], fabsf(sv[c]), fabsf(sv[c + 1]));
-        const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-        if (__all_sync(FULL, row_lo >= row_hi || top * fabsf(a.cap_in) <= 1.f)) {
-          const CapPoly<QT> cap(a.cap_log2);
-          const uint64_t in2 = f2splat(a.cap_in);
-#pragma unroll
-          for (int c = 0; c < kBN; c += 2) {
-            const float2 x = f2unpack(cap(f2mul(f2pack(sv[c], sv[c + 1]), in2)));
-            sv[c] = x.x;
-            sv[c + 1] = x.y;
-          }
-        } else {                             // some score past the cap: tanh over its range
-#pragma unroll
-          for (int c = 0; c < kBN; ++c) sv[c] = a.cap_log2 * tanh_f32(sv[c] * a.cap_in);
+          for (int e = 0; e < 32; ++e) sv[32 * i + e] = v[e];
         }
-        factor = 1.f;
-      }
-      if constexpr (BIAS) {
-        // -slope |pos - t| is linear in the column on either side of pos
-        const int d0 = t_base - row_pos;     // column c is at distance |c + d0|
-        const bool before = d0 + kBN - 1 <= 0, after = d0 >= 0;
-        const bool off = row_lo >= row_hi;
-        const uint64_t f2 = f2splat(factor);
-        if (__all_sync(FULL, off || before) || __all_sync(FULL, off || after)) {
-          const float sg = before ? slope : -slope;
+        tmem_wait_ld();
+        const int t_base = (t_lo + j) * kBN + half_me * NC;  // the token of column 0
+        const bool full = row_lo <= t_base && row_hi >= t_base + NC;
+        const int nvalid = row_hi - t_base, nskip = row_lo - t_base;   // [nskip, nvalid) are seen
+        float factor = a.scale_log2;         // what turns sv into scores in log2 units
+        if constexpr (CAP) {
+          float big[2] = {0.f, 0.f};
 #pragma unroll
-          for (int c32 = 0; c32 < kBN; c32 += 32) {
-            const float b0 = sg * static_cast<float>(d0 + c32);
-            uint64_t b = f2pack(b0, b0 + sg);
-            const uint64_t step = f2splat(2.f * sg);
+          for (int c = 0; c < NC; c += 2)
+            big[(c >> 1) & 1] = fmax3(big[(c >> 1) & 1], fabsf(sv[c]), fabsf(sv[c + 1]));
+          if (__all_sync(FULL, row_lo >= row_hi ||
+                                   fmaxf(big[0], big[1]) * fabsf(a.cap_in) <= 1.f)) {
+            const CapPoly<QT> cap(a.cap_log2);
+            const uint64_t in2 = f2splat(a.cap_in);
 #pragma unroll
-            for (int c = c32; c < c32 + 32; c += 2) {
-              const float2 x = f2unpack(f2fma(f2pack(sv[c], sv[c + 1]), f2, b));
-              sv[c] = x.x;
-              sv[c + 1] = x.y;
-              b = f2add(b, step);
+            for (int c = 0; c < NC; c += 2) {
+              const float2 y = f2unpack(cap(f2mul(f2pack(sv[c], sv[c + 1]), in2)));
+              sv[c] = y.x;
+              sv[c + 1] = y.y;
             }
-          }
-        } else {
-          const float d = static_cast<float>(d0);
+          } else {                           // some score past the cap: tanh over its range
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            sv[c] = fmaf(-slope, fabsf(d + static_cast<float>(c)), sv[c] * factor);
+            for (int c = 0; c < NC; ++c) sv[c] = a.cap_log2 * tanh_f32(sv[c] * a.cap_in);
+          }
+          factor = 1.f;
         }
-        factor = 1.f;
-      }
-      auto seen = [&](int c) { return c < nvalid && (!MASK || c >= nskip); };
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (full && factor >= 0.f) {
+        if constexpr (BIAS) {
+          // -slope |pos - t| is linear in the column on either side of pos
+          const int d0 = t_base - row_pos;   // column c is at distance |c + d0|
+          const bool before = d0 + NC - 1 <= 0, after = d0 >= 0;
+          const bool off = row_lo >= row_hi;
+          const uint64_t f2 = f2splat(factor);
+          if (__all_sync(FULL, off || before) || __all_sync(FULL, off || after)) {
+            const float sg = before ? slope : -slope;
 #pragma unroll
-        for (int c = 0; c < kBN; c += 2)
-          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
-      } else if (full) {
+            for (int c32 = 0; c32 < NC; c32 += 32) {
+              const float b0 = sg * static_cast<float>(d0 + c32);
+              uint64_t b = f2pack(b0, b0 + sg);
+              const uint64_t step = f2splat(2.f * sg);
 #pragma unroll
-        for (int c = 0; c < kBN; c += 2)
-          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], -sv[c], -sv[c + 1]);
-      } else {
-        const float sg = factor >= 0.f ? 1.f : -1.f;
+              for (int c = c32; c < c32 + 32; c += 2) {
+                const float2 y = f2unpack(f2fma(f2pack(sv[c], sv[c + 1]), f2, b));
+                sv[c] = y.x;
+                sv[c + 1] = y.y;
+                b = f2add(b, step);
+              }
+            }
+          } else {
+            const float d = static_cast<float>(d0);
 #pragma unroll
-        for (int c = 0; c < kBN; ++c) mx[c & 3] = fmaxf(mx[c & 3], seen(c) ? sg * sv[c] : -INFINITY);
-      }
-      const float rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // the exponent base moves only when the tile's max exceeds it by more
-      // than 8 (log2 units): p <= 2^8 stays exact enough in 16 bits, O and l
-      // share the base, and O / l is unchanged
-      const float tmax = rmax == -INFINITY ? -INFINITY : rmax * fabsf(factor);
-      const float m_new = tmax > m_run + 8.f ? tmax : m_run;
-      const float base = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = m_new == m_run ? 1.f : fast_exp2(m_run - base);
-      // P = 2^(scale * s - base) over the S columns just read (masked
-      // columns 0), pairs in packed f32x2 arithmetic: 32 tokens per
-      // 16-column store
-      const uint64_t sc2 = f2splat(factor), nb2 = f2splat(-base);
-      uint64_t ps2[2] = {f2splat(0.f), f2splat(0.f)};
-#pragma unroll
-      for (int c32 = 0; c32 < kBN / 32; ++c32) {
-        uint32_t hw[16], lw[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c = 32 * c32 + 2 * e;
-          const uint64_t x2 = f2fma(f2pack(sv[c], sv[c + 1]), sc2, nb2);
-          const float2 xx = f2unpack(x2);
-          float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
-          if (!full) {
-            p.x = seen(c) ? p.x : 0.f;
-            p.y = seen(c + 1) ? p.y : 0.f;
+            for (int c = 0; c < NC; ++c)
+              sv[c] = fmaf(-slope, fabsf(d + static_cast<float>(c)), sv[c] * factor);
           }
-          ps2[e & 1] = f2add(ps2[e & 1], f2pack(p.x, p.y));
-          hw[e] = pack2<QT>(p.x, p.y);
-          if constexpr (PARTS == 2) {
+          factor = 1.f;
+        }
+        auto seen = [&](int c) { return c < nvalid && c >= nskip; };
+        const float sg = factor >= 0.f ? 1.f : -1.f;
+        float mx[2] = {-INFINITY, -INFINITY};
+        if (full && factor >= 0.f) {
+#pragma unroll
+          for (int c = 0; c < NC; c += 2)
+            mx[(c >> 1) & 1] = fmax3(mx[(c >> 1) & 1], sv[c], sv[c + 1]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+            mx[c & 1] = fmaxf(mx[c & 1], full || seen(c) ? sg * sv[c] : -INFINITY);
+        }
+        // the exponent base is a whole number at or above the row's maximum, moved only
+        // when that exceeds it by more than 8.  A maximum past +-32767 ends in a row
+        // without a finite positive sum, which is computed again below.
+        const float top = fmaxf(mx[0], mx[1]);
+        const int top_i = top == -INFINITY
+                              ? kNone : max(-32767, min(32767, __float2int_ru(top * fabsf(factor))));
+        pair_max[mine] = static_cast<int16_t>(top_i);
+        mbar_arrive(bar(kBarPair + pair));
+        if (!mbar_wait_abortable(bar(kBarPair + pair), j & 1, a.timeout_ns, abort)) break;
+        const int both = max(top_i, static_cast<int>(pair_max[other]));
+        const float tmax = both == kNone ? -INFINITY : static_cast<float>(both);
+        const float m_new = tmax > m_run + 8.f ? tmax : m_run;
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = m_new == m_run ? 1.f : fast_exp2(m_run - base);
+        const uint64_t sc2 = f2splat(factor), nb2 = f2splat(-base);
+        uint64_t ps2[2] = {f2splat(0.f), f2splat(0.f)};
+#pragma unroll
+        for (int c32 = 0; c32 < NC / 32; ++c32) {
+          uint32_t hw[16], lw[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = 32 * c32 + 2 * e;
+            const float2 xx = f2unpack(f2fma(f2pack(sv[c], sv[c + 1]), sc2, nb2));
+            float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+            if (!full) {
+              p.x = seen(c) ? p.x : 0.f;
+              p.y = seen(c + 1) ? p.y : 0.f;
+            }
+            ps2[e & 1] = f2add(ps2[e & 1], f2pack(p.x, p.y));
+            hw[e] = pack2<QT>(p.x, p.y);
             const float2 f = unpack2<QT>(hw[e]);
             lw[e] = pack2<QT>(p.x - f.x, p.y - f.y);
           }
+          tmem_st16(s_col + 32 * c32, hw);
+          tmem_st16(s_col + 32 * c32 + 16, lw);
         }
-        tmem_st16(t_s(x) + lane_off + 16 * c32, hw);
-        if constexpr (PARTS == 2) tmem_st16(t_s(x) + lane_off + 64 + 16 * c32, lw);
-      }
-      const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
-      l_run = l_run * alpha + ((s0.x + s0.y) + (s1.x + s1.y));
-      m_run = m_new;
-      if (j > 0 && __any_sync(FULL, alpha != 1.f)) {
+        const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
+        l_run = l_run * alpha + ((s0.x + s0.y) + (s1.x + s1.y));
+        m_run = m_new;
+        if (j > 0 && __any_sync(FULL, alpha != 1.f)) {       // each thread half of the row's O
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 4 / HALVES; ++i) {
+            const uint32_t o_col = t_o(x) + lane_off + static_cast<uint32_t>(half_me * 64 + 32 * i);
+            float v[32];
+            tmem_ld32(o_col, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= alpha;
+            tmem_st32(o_col, v);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(bar(kBarPFull + x));
+      }
+    } else {
+      for (int j = 0; j < ntiles; ++j) {
+        // S_x(j) complete also means PV_x(j-1) is: its MMA waited for that
+        if (!mbar_wait_abortable(bar(kBarSFull + x), j & 1, a.timeout_ns, abort)) break;
+        tc_fence_after_sync();
+        float sv[kBN];
+#pragma unroll
+        for (int i = 0; i < kBN / 32; ++i) {
           float v[32];
-          tmem_ld32(t_o(x) + lane_off + 32 * i, v);
-          tmem_wait_ld();
+          tmem_ld32(t_s(x) + lane_off + 32 * i, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= alpha;
-          tmem_st32(t_o(x) + lane_off + 32 * i, v);
+          for (int e = 0; e < 32; ++e) sv[32 * i + e] = v[e];
         }
+        tmem_wait_ld();
+
+        // the row max of scale * s (log2 units), taken on the raw dot products:
+        // the largest for scale >= 0, the smallest otherwise; four independent
+        // chains; no per-element mask on a tile that lies wholly inside this
+        // row's causal window
+        const int t_base = (t_lo + j) * kBN;
+        const bool full = t_base + kBN - 1 <= pos;
+        const int nvalid = full ? kBN : max(0, pos - t_base + 1);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (full && a.scale_log2 >= 0.f) {
+#pragma unroll
+          for (int c = 0; c < kBN; c += 2)
+            mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+        } else if (full) {
+#pragma unroll
+          for (int c = 0; c < kBN; c += 2)
+            mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], -sv[c], -sv[c + 1]);
+        } else {
+          const float sg = a.scale_log2 >= 0.f ? 1.f : -1.f;
+#pragma unroll
+          for (int c = 0; c < kBN; ++c) mx[c & 3] = fmaxf(mx[c & 3], c < nvalid ? sg * sv[c] : -INFINITY);
+        }
+        const float rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // the exponent base moves only when the tile's max exceeds it by more
+        // than 8 (log2 units): p <= 2^8 stays exact enough in 16 bits, O and l
+        // share the base, and O / l is unchanged
+        const float tmax = rmax == -INFINITY ? -INFINITY : rmax * fabsf(a.scale_log2);
+        const float m_new = tmax > m_run + 8.f ? tmax : m_run;
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = m_new == m_run ? 1.f : fast_exp2(m_run - base);
+        // P = 2^(scale * s - base) over the S columns just read (masked
+        // columns 0), pairs in packed f32x2 arithmetic: 32 tokens per
+        // 16-column store
+        const uint64_t sc2 = f2splat(a.scale_log2), nb2 = f2splat(-base);
+        uint64_t ps2[2] = {f2splat(0.f), f2splat(0.f)};
+#pragma unroll
+        for (int c32 = 0; c32 < kBN / 32; ++c32) {
+          uint32_t hw[16], lw[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = 32 * c32 + 2 * e;
+            const uint64_t x2 = f2fma(f2pack(sv[c], sv[c + 1]), sc2, nb2);
+            const float2 xx = f2unpack(x2);
+            float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+            if (!full) {
+              p.x = c < nvalid ? p.x : 0.f;
+              p.y = c + 1 < nvalid ? p.y : 0.f;
+            }
+            ps2[e & 1] = f2add(ps2[e & 1], f2pack(p.x, p.y));
+            hw[e] = pack2<QT>(p.x, p.y);
+            if constexpr (PARTS == 2) {
+              const float2 f = unpack2<QT>(hw[e]);
+              lw[e] = pack2<QT>(p.x - f.x, p.y - f.y);
+            }
+          }
+          tmem_st16(t_s(x) + lane_off + 16 * c32, hw);
+          if constexpr (PARTS == 2) tmem_st16(t_s(x) + lane_off + 64 + 16 * c32, lw);
+        }
+        const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
+        l_run = l_run * alpha + ((s0.x + s0.y) + (s1.x + s1.y));
+        m_run = m_new;
+        if (j > 0 && __any_sync(FULL, alpha != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v[32];
+            tmem_ld32(t_o(x) + lane_off + 32 * i, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= alpha;
+            tmem_st32(t_o(x) + lane_off + 32 * i, v);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(bar(kBarPFull + x));
       }
-      tmem_wait_st();
-      tc_fence_before_sync();
-      mbar_arrive(bar(kBarPFull + x));
     }
     if (ntiles > 0)
       mbar_wait_abortable(bar(kBarODone + x), (ntiles - 1) & 1, a.timeout_ns, abort);
@@ -666,25 +778,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(bar(kBarDrain), 0, kDrainLimitNs);
     }
   }
+  // MASK: each thread's l for the row's other thread, over the (consumed) query tiles
+  float* pair_l = reinterpret_cast<float*>(smem_raw + (sbase - sraw));
+  if (MASK && warp < NSM) pair_l[(x_me * 2 + half_me) * kRows + row_me] = l_run;
   __syncthreads();                           // drains done
   tc_fence_after_sync();
   const bool dead = *abort;
   const bool empty = ntiles == 0;            // an empty split: m = -inf, l = 0, o = 0
-  if (warp < 8) {
+  bool odd = false;                          // MASK: a non-finite value in this thread's part
+  if (warp < NSM) {
     // ---- epilogue: out row = O / l (cascade: the partial o / l, m, l)
     const int x = x_me;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    if constexpr (MASK) l_run += pair_l[(x * 2 + 1 - half_me) * kRows + row_me];
     const float inv = (!dead && l_run > 0.f) ? 1.f / l_run : 0.f;
     const int h = kvh * G + row_me % G;
     const size_t orow_idx = static_cast<size_t>(q0 + tok_me) * a.num_heads + h;
-    bool odd = false;                        // MASK: a non-finite value in this row
     const size_t split_rows = cascade ? static_cast<size_t>(seq) * q_len * a.num_heads : 0;
     if (cascade && row_valid) {
       a.part_m[split_rows + orow_idx] = (dead || empty) ? -INFINITY : m_run;
       a.part_l[split_rows + orow_idx] = (dead || empty) ? 0.f : l_run;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int ih = 0; ih < 4 / HALVES; ++ih) {
+      const int i = MASK ? half_me * (4 / HALVES) + ih : ih;
       float v[32];
       tmem_ld32(t_o(x) + lane_off + 32 * i, v);
       tmem_wait_ld();
@@ -697,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float s = 0.f;                       // 0 * inf and 0 * NaN are NaN
 #pragma unroll
         for (int e = 0; e < 32; ++e) s = fmaf(0.f, v[e], s);
-        odd = odd || !(s == 0.f) || !(l_run < INFINITY);
+        odd = odd || !(s == 0.f) || !(l_run < INFINITY) || (row_lo < row_hi && !(l_run > 0.f));
       }
       if (cascade) {
         float4* dst = reinterpret_cast<float4*>(a.part_o + (split_rows + orow_idx) * kD + 32 * i);
@@ -718,20 +835,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if constexpr (MASK) {
-      uint32_t again = __ballot_sync(FULL, odd && !dead && row_valid);
+    if constexpr (MASK)
+      pair_l[512 + (x_me * 2 + half_me) * kRows + row_me] = odd && !dead && row_valid ? 1.f : 0.f;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if constexpr (MASK) {                      // the rows that came out non-finite, once more
+    if (warp < NSM && half_me == 0) {
+      const float* flag = pair_l + 512 + x_me * 2 * kRows + row_me;
+      uint32_t again = __ballot_sync(FULL, flag[0] != 0.f || flag[kRows] != 0.f);
       while (again) {
         const int src = __ffs(again) - 1;
         again &= again - 1;
-        masked_row<QT>(a, table, __shfl_sync(FULL, q0 + tok_me, src), __shfl_sync(FULL, h, src), kvh,
+        masked_row<QT>(a, table, __shfl_sync(FULL, q0 + tok_me, src),
+                       __shfl_sync(FULL, kvh * G + row_me % G, src), kvh,
                        __shfl_sync(FULL, row_pos, src), __shfl_sync(FULL, row_lo, src),
                        __shfl_sync(FULL, row_hi, src));
       }
     }
   }
-  tc_fence_before_sync();
-  __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 cudaError_t make_q_map(CUtensorMap* map, const void* q, int total_q, int num_heads, int G) {
