@@ -166,12 +166,12 @@ struct CapPoly {
 #pragma unroll
     for (int i = 0; i < N; ++i) c[i] = f2splat(factor * (N == 5 ? k4[i % 5] : k5[i]));
   }
-  __device__ __forceinline__ uint64_t operator()(uint64_t y) const {
+  __device__ __forceinline__ uint64_t operator()(uint64_t y, uint64_t add) const {
     const uint64_t z = f2mul(y, y);
     uint64_t q = c[N - 1];
 #pragma unroll
     for (int i = N - 2; i >= 0; --i) q = f2fma(q, z, c[i]);
-    return f2mul(q, y);
+    return f2fma(q, y, add);
   }
 };
 
@@ -546,110 +546,165 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         }
         tmem_wait_ld();
         const int t_base = (t_lo + j) * kBN + half_me * NC;  // the token of column 0
-        const bool full = row_lo <= t_base && row_hi >= t_base + NC;
-        const int nvalid = row_hi - t_base, nskip = row_lo - t_base;   // [nskip, nvalid) are seen
+        const bool off = row_lo >= row_hi;   // this row sees nothing
+        // every column seen by every row of the warp; else a bit per seen column (a test
+        // of two bounds per element would cost as much as the rest of the softmax)
+        const bool full = __all_sync(FULL, !row_valid || (row_lo <= t_base && row_hi >= t_base + NC));
+        uint32_t bits[NC / 32];
+#pragma unroll
+        for (int i = 0; i < NC / 32; ++i) {
+          const int from = max(0, min(32, row_lo - t_base - 32 * i));
+          const int to = max(0, min(32, row_hi - t_base - 32 * i));
+          bits[i] = from < to ? (FULL >> (32 - (to - from))) << from : 0u;
+        }
+        auto seen = [&](int c) { return ((bits[c / 32] >> (c % 32)) & 1u) != 0; };
+
+        // The usual tile: the cap as a polynomial (every |score| within the cap's unit
+        // range), the bias linear in the column (all of the tile on one side of pos).
+        // Else the scores are changed in place, element by element, and `factor` is 1.
+        const int d0 = t_base - row_pos;     // column c is at distance |c + d0|
         float factor = a.scale_log2;         // what turns sv into scores in log2 units
+        bool usual = true;
         if constexpr (CAP) {
           float big[2] = {0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < NC; c += 2)
             big[(c >> 1) & 1] = fmax3(big[(c >> 1) & 1], fabsf(sv[c]), fabsf(sv[c + 1]));
-          if (__all_sync(FULL, row_lo >= row_hi ||
-                                   fmaxf(big[0], big[1]) * fabsf(a.cap_in) <= 1.f)) {
-            const CapPoly<QT> cap(a.cap_log2);
-            const uint64_t in2 = f2splat(a.cap_in);
-#pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-              const float2 y = f2unpack(cap(f2mul(f2pack(sv[c], sv[c + 1]), in2)));
-              sv[c] = y.x;
-              sv[c + 1] = y.y;
-            }
-          } else {                           // some score past the cap: tanh over its range
-#pragma unroll
-            for (int c = 0; c < NC; ++c) sv[c] = a.cap_log2 * tanh_f32(sv[c] * a.cap_in);
-          }
-          factor = 1.f;
+          usual = off || fmaxf(big[0], big[1]) * fabsf(a.cap_in) <= 1.f;
         }
+        bool before = true;
         if constexpr (BIAS) {
-          // -slope |pos - t| is linear in the column on either side of pos
-          const int d0 = t_base - row_pos;   // column c is at distance |c + d0|
-          const bool before = d0 + NC - 1 <= 0, after = d0 >= 0;
-          const bool off = row_lo >= row_hi;
-          const uint64_t f2 = f2splat(factor);
-          if (__all_sync(FULL, off || before) || __all_sync(FULL, off || after)) {
-            const float sg = before ? slope : -slope;
+          before = d0 + NC - 1 <= 0;
+          usual = usual && (off || before || d0 >= 0);
+        }
+        usual = (!CAP && !BIAS) || __all_sync(FULL, usual);
+        if (!usual) {
+          const float dist = static_cast<float>(d0);
 #pragma unroll
-            for (int c32 = 0; c32 < NC; c32 += 32) {
-              const float b0 = sg * static_cast<float>(d0 + c32);
-              uint64_t b = f2pack(b0, b0 + sg);
-              const uint64_t step = f2splat(2.f * sg);
-#pragma unroll
-              for (int c = c32; c < c32 + 32; c += 2) {
-                const float2 y = f2unpack(f2fma(f2pack(sv[c], sv[c + 1]), f2, b));
-                sv[c] = y.x;
-                sv[c + 1] = y.y;
-                b = f2add(b, step);
-              }
-            }
-          } else {
-            const float d = static_cast<float>(d0);
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              sv[c] = fmaf(-slope, fabsf(d + static_cast<float>(c)), sv[c] * factor);
+          for (int c = 0; c < NC; ++c) {
+            float y = CAP ? a.cap_log2 * tanh_f32(sv[c] * a.cap_in) : sv[c] * a.scale_log2;
+            if constexpr (BIAS) y = fmaf(-slope, fabsf(dist + static_cast<float>(c)), y);
+            sv[c] = y;
           }
           factor = 1.f;
         }
-        auto seen = [&](int c) { return c < nvalid && c >= nskip; };
-        const float sg = factor >= 0.f ? 1.f : -1.f;
+
+        // The row's maximum, or in the usual tile what the cap makes of the largest product
+        // with no bias (which only lowers it): enough to tell whether the base has to move.
+        const float dir = !CAP || !usual ? factor : a.cap_in;
         float mx[2] = {-INFINITY, -INFINITY};
-        if (full && factor >= 0.f) {
+        if (full && dir >= 0.f) {
 #pragma unroll
           for (int c = 0; c < NC; c += 2)
             mx[(c >> 1) & 1] = fmax3(mx[(c >> 1) & 1], sv[c], sv[c + 1]);
         } else {
+          const float sg = dir >= 0.f ? 1.f : -1.f;    // (bits cover a whole tile too)
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            mx[c & 1] = fmaxf(mx[c & 1], full || seen(c) ? sg * sv[c] : -INFINITY);
+            mx[c & 1] = fmaxf(mx[c & 1], seen(c) ? sg * sv[c] : -INFINITY);
         }
+        float top = fmaxf(mx[0], mx[1]);
+        if (top != -INFINITY)
+          top = CAP && usual ? a.cap_log2 * tanh_f32(top * fabsf(a.cap_in)) : top * fabsf(factor);
         // the exponent base is a whole number at or above the row's maximum, moved only
         // when that exceeds it by more than 8.  A maximum past +-32767 ends in a row
         // without a finite positive sum, which is computed again below.
-        const float top = fmaxf(mx[0], mx[1]);
-        const int top_i = top == -INFINITY
-                              ? kNone : max(-32767, min(32767, __float2int_ru(top * fabsf(factor))));
+        const int top_i = top == -INFINITY ? kNone : max(-32767, min(32767, __float2int_ru(top)));
         pair_max[mine] = static_cast<int16_t>(top_i);
         mbar_arrive(bar(kBarPair + pair));
-        if (!mbar_wait_abortable(bar(kBarPair + pair), j & 1, a.timeout_ns, abort)) break;
-        const int both = max(top_i, static_cast<int>(pair_max[other]));
-        const float tmax = both == kNone ? -INFINITY : static_cast<float>(both);
-        const float m_new = tmax > m_run + 8.f ? tmax : m_run;
-        const float base = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = m_new == m_run ? 1.f : fast_exp2(m_run - base);
-        const uint64_t sc2 = f2splat(factor), nb2 = f2splat(-base);
-        uint64_t ps2[2] = {f2splat(0.f), f2splat(0.f)};
-#pragma unroll
-        for (int c32 = 0; c32 < NC / 32; ++c32) {
-          uint32_t hw[16], lw[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c = 32 * c32 + 2 * e;
-            const float2 xx = f2unpack(f2fma(f2pack(sv[c], sv[c + 1]), sc2, nb2));
-            float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
-            if (!full) {
-              p.x = seen(c) ? p.x : 0.f;
-              p.y = seen(c + 1) ? p.y : 0.f;
-            }
-            ps2[e & 1] = f2add(ps2[e & 1], f2pack(p.x, p.y));
-            hw[e] = pack2<QT>(p.x, p.y);
-            const float2 f = unpack2<QT>(hw[e]);
-            lw[e] = pack2<QT>(p.x - f.x, p.y - f.y);
+
+        // With no maximum of its own past the base, a warp goes on at the base as it
+        // stands while the row's other thread gets to its maximum; should that move the
+        // base, P is scaled afterwards (by a power of two: the base is whole).
+        auto wait_pair = [&]() {
+          return mbar_wait_abortable(bar(kBarPair + pair), j & 1, a.timeout_ns, abort);
+        };
+        float alpha = 1.f;                   // what a move of the base makes of l and O
+        auto move_base = [&]() {
+          const int both = max(top_i, static_cast<int>(pair_max[other]));
+          const float tmax = both == kNone ? -INFINITY : static_cast<float>(both);
+          if (tmax > m_run + 8.f) {
+            alpha = fast_exp2(m_run - tmax);
+            m_run = tmax;
           }
-          tmem_st16(s_col + 32 * c32, hw);
-          tmem_st16(s_col + 32 * c32 + 16, lw);
+        };
+        const bool first = __any_sync(FULL, !off && (m_run == -INFINITY || (top_i != kNone &&
+                                            static_cast<float>(top_i) > m_run + 8.f)));
+        if (first) {
+          if (!wait_pair()) break;
+          move_base();
         }
+        uint64_t ps2[2];
+        auto emit = [&](auto poly, auto whole, float base) {
+          constexpr bool POLY = decltype(poly)::value;       // the usual tile's changes
+          constexpr bool WHOLE = decltype(whole)::value;     // every column is seen
+          const CapPoly<QT> cap(a.cap_log2);
+          const uint64_t sc2 = f2splat(CAP && POLY ? a.cap_in : factor), nb2 = f2splat(-base);
+          const float sg = before ? slope : -slope;
+          ps2[0] = ps2[1] = f2splat(0.f);
+#pragma unroll
+          for (int c32 = 0; c32 < NC / 32; ++c32) {
+            uint32_t hw[16], lw[16];
+            uint64_t b = nb2;
+            const uint64_t step = f2splat(2.f * sg);
+            if constexpr (BIAS && POLY) {
+              const float b0 = sg * static_cast<float>(d0 + 32 * c32);
+              b = f2add(f2pack(b0, b0 + sg), nb2);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int c = 32 * c32 + 2 * e;
+              const uint64_t s2 = f2pack(sv[c], sv[c + 1]);
+              const float2 xx = f2unpack(CAP && POLY ? cap(f2mul(s2, sc2), b) : f2fma(s2, sc2, b));
+              if constexpr (BIAS && POLY) b = f2add(b, step);
+              float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+              if constexpr (!WHOLE) {
+                p.x = seen(c) ? p.x : 0.f;
+                p.y = seen(c + 1) ? p.y : 0.f;
+              }
+              ps2[e & 1] = f2add(ps2[e & 1], f2pack(p.x, p.y));
+              hw[e] = pack2<QT>(p.x, p.y);
+              const float2 f = unpack2<QT>(hw[e]);
+              lw[e] = pack2<QT>(p.x - f.x, p.y - f.y);
+            }
+            tmem_st16(s_col + 32 * c32, hw);
+            tmem_st16(s_col + 32 * c32 + 16, lw);
+          }
+        };
+        const float base = m_run == -INFINITY ? 0.f : m_run;
+        using Yes = std::true_type;
+        using No = std::false_type;
+        if ((CAP || BIAS) && usual) full ? emit(Yes{}, Yes{}, base) : emit(Yes{}, No{}, base);
+        else full ? emit(No{}, Yes{}, base) : emit(No{}, No{}, base);
         const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
-        l_run = l_run * alpha + ((s0.x + s0.y) + (s1.x + s1.y));
-        m_run = m_new;
+        float sum = (s0.x + s0.y) + (s1.x + s1.y);
+        if (!first) {
+          if (!wait_pair()) break;
+          move_base();
+          if (__any_sync(FULL, alpha != 1.f)) {
+            sum *= alpha;
+            tmem_wait_st();
+#pragma unroll 1
+            for (int c32 = 0; c32 < NC / 32; ++c32) {
+              float v[32];
+              tmem_ld32(s_col + 32 * c32, v);
+              tmem_wait_ld();
+              uint32_t hw[16], lw[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 h = unpack2<QT>(__float_as_uint(v[e]));
+                const float2 l = unpack2<QT>(__float_as_uint(v[16 + e]));
+                const float2 p = make_float2((h.x + l.x) * alpha, (h.y + l.y) * alpha);
+                hw[e] = pack2<QT>(p.x, p.y);
+                const float2 f = unpack2<QT>(hw[e]);
+                lw[e] = pack2<QT>(p.x - f.x, p.y - f.y);
+              }
+              tmem_st16(s_col + 32 * c32, hw);
+              tmem_st16(s_col + 32 * c32 + 16, lw);
+            }
+          }
+        }
+        l_run = l_run * alpha + sum;
         if (j > 0 && __any_sync(FULL, alpha != 1.f)) {       // each thread half of the row's O
 #pragma unroll
           for (int i = 0; i < 4 / HALVES; ++i) {
