@@ -135,10 +135,22 @@ __device__ __forceinline__ uint64_t f2mul(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t f2sub(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t f2splat(float v) { return f2pack(v, v); }
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The largest magnitude of three (an fabsf of an asm operand would be an instruction).
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -561,15 +573,14 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
 
         // The usual tile: the cap as a polynomial (every |score| within the cap's unit
         // range), the bias linear in the column (all of the tile on one side of pos).
-        // Else the scores are changed in place, element by element, and `factor` is 1.
+        // Else the scores are changed element by element.
         const int d0 = t_base - row_pos;     // column c is at distance |c + d0|
-        float factor = a.scale_log2;         // what turns sv into scores in log2 units
         bool usual = true;
         if constexpr (CAP) {
           float big[2] = {0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < NC; c += 2)
-            big[(c >> 1) & 1] = fmax3(big[(c >> 1) & 1], fabsf(sv[c]), fabsf(sv[c + 1]));
+            big[(c >> 1) & 1] = fmax3_abs(big[(c >> 1) & 1], sv[c], sv[c + 1]);
           usual = off || fmaxf(big[0], big[1]) * fabsf(a.cap_in) <= 1.f;
         }
         bool before = true;
@@ -578,34 +589,37 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
           usual = usual && (off || before || d0 >= 0);
         }
         usual = (!CAP && !BIAS) || __all_sync(FULL, usual);
-        if (!usual) {
-          const float dist = static_cast<float>(d0);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            float y = CAP ? a.cap_log2 * tanh_f32(sv[c] * a.cap_in) : sv[c] * a.scale_log2;
-            if constexpr (BIAS) y = fmaf(-slope, fabsf(dist + static_cast<float>(c)), y);
-            sv[c] = y;
-          }
-          factor = 1.f;
-        }
+        // one score of an unusual tile, in log2 units (column c)
+        auto score = [&](float v, int c) {
+          float y = CAP ? a.cap_log2 * tanh_f32(v * a.cap_in) : v * a.scale_log2;
+          if constexpr (BIAS) y = fmaf(-slope, fabsf(static_cast<float>(d0 + c)), y);
+          return y;
+        };
 
         // The row's maximum, or in the usual tile what the cap makes of the largest product
         // with no bias (which only lowers it): enough to tell whether the base has to move.
-        const float dir = !CAP || !usual ? factor : a.cap_in;
-        float mx[2] = {-INFINITY, -INFINITY};
-        if (full && dir >= 0.f) {
+        float mx[2] = {-INFINITY, -INFINITY}, top;
+        if (usual) {
+          const float dir = CAP ? a.cap_in : a.scale_log2;
+          if (full && dir >= 0.f) {
 #pragma unroll
-          for (int c = 0; c < NC; c += 2)
-            mx[(c >> 1) & 1] = fmax3(mx[(c >> 1) & 1], sv[c], sv[c + 1]);
+            for (int c = 0; c < NC; c += 2)
+              mx[(c >> 1) & 1] = fmax3(mx[(c >> 1) & 1], sv[c], sv[c + 1]);
+          } else {
+            const float sg = dir >= 0.f ? 1.f : -1.f;    // (bits cover a whole tile too)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              mx[c & 1] = fmaxf(mx[c & 1], seen(c) ? sg * sv[c] : -INFINITY);
+          }
+          top = fmaxf(mx[0], mx[1]);
+          if (top != -INFINITY)
+            top = CAP ? a.cap_log2 * tanh_f32(top * fabsf(a.cap_in)) : top * fabsf(a.scale_log2);
         } else {
-          const float sg = dir >= 0.f ? 1.f : -1.f;    // (bits cover a whole tile too)
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            mx[c & 1] = fmaxf(mx[c & 1], seen(c) ? sg * sv[c] : -INFINITY);
+            mx[c & 1] = fmaxf(mx[c & 1], seen(c) ? score(sv[c], c) : -INFINITY);
+          top = fmaxf(mx[0], mx[1]);
         }
-        float top = fmaxf(mx[0], mx[1]);
-        if (top != -INFINITY)
-          top = CAP && usual ? a.cap_log2 * tanh_f32(top * fabsf(a.cap_in)) : top * fabsf(factor);
         // the exponent base is a whole number at or above the row's maximum, moved only
         // when that exceeds it by more than 8.  A maximum past +-32767 ends in a row
         // without a finite positive sum, which is computed again below.
@@ -636,14 +650,19 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         }
         uint64_t ps2[2];
         auto emit = [&](auto poly, auto whole, float base) {
-          constexpr bool POLY = decltype(poly)::value;       // the usual tile's changes
+          constexpr bool POLY = decltype(poly)::value;       // a usual tile
           constexpr bool WHOLE = decltype(whole)::value;     // every column is seen
           const CapPoly<QT> cap(a.cap_log2);
-          const uint64_t sc2 = f2splat(CAP && POLY ? a.cap_in : factor), nb2 = f2splat(-base);
+          const uint64_t sc2 = f2splat(CAP ? a.cap_in : a.scale_log2), nb2 = f2splat(-base);
           const float sg = before ? slope : -slope;
           ps2[0] = ps2[1] = f2splat(0.f);
 #pragma unroll
           for (int c32 = 0; c32 < NC / 32; ++c32) {
+            // the products once more: kept from the first pass, they and the 32 words of P
+            // would not fit 96 registers
+            float sv[32];
+            tmem_ld32(s_col + 32 * c32, sv);
+            tmem_wait_ld();
             uint32_t hw[16], lw[16];
             uint64_t b = nb2;
             const uint64_t step = f2splat(2.f * sg);
@@ -654,18 +673,25 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int c = 32 * c32 + 2 * e;
-              const uint64_t s2 = f2pack(sv[c], sv[c + 1]);
-              const float2 xx = f2unpack(CAP && POLY ? cap(f2mul(s2, sc2), b) : f2fma(s2, sc2, b));
-              if constexpr (BIAS && POLY) b = f2add(b, step);
+              const uint64_t s2 = f2pack(sv[2 * e], sv[2 * e + 1]);
+              float2 xx;
+              if constexpr (POLY) {
+                xx = f2unpack(CAP ? cap(f2mul(s2, sc2), b) : f2fma(s2, sc2, b));
+                if constexpr (BIAS) b = f2add(b, step);
+              } else {
+                xx = make_float2(score(sv[2 * e], c) - base, score(sv[2 * e + 1], c + 1) - base);
+              }
               float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
               if constexpr (!WHOLE) {
                 p.x = seen(c) ? p.x : 0.f;
                 p.y = seen(c + 1) ? p.y : 0.f;
               }
-              ps2[e & 1] = f2add(ps2[e & 1], f2pack(p.x, p.y));
+              const uint64_t p2 = f2pack(p.x, p.y);
+              ps2[e & 1] = f2add(ps2[e & 1], p2);
               hw[e] = pack2<QT>(p.x, p.y);
               const float2 f = unpack2<QT>(hw[e]);
-              lw[e] = pack2<QT>(p.x - f.x, p.y - f.y);
+              const float2 rest = f2unpack(f2sub(p2, f2pack(f.x, f.y)));
+              lw[e] = pack2<QT>(rest.x, rest.y);
             }
             tmem_st16(s_col + 32 * c32, hw);
             tmem_st16(s_col + 32 * c32 + 16, lw);
@@ -674,8 +700,8 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         const float base = m_run == -INFINITY ? 0.f : m_run;
         using Yes = std::true_type;
         using No = std::false_type;
-        if ((CAP || BIAS) && usual) full ? emit(Yes{}, Yes{}, base) : emit(Yes{}, No{}, base);
-        else full ? emit(No{}, Yes{}, base) : emit(No{}, No{}, base);
+        if (usual) full ? emit(Yes{}, Yes{}, base) : emit(Yes{}, No{}, base);
+        else emit(No{}, No{}, base);
         const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
         float sum = (s0.x + s0.y) + (s1.x + s1.y);
         if (!first) {
