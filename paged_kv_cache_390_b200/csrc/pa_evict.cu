@@ -28,9 +28,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKeys = 4096;                    // keys a CTA holds; longer runs are read again
+constexpr int kKeys = 8192;                    // keys a CTA holds; longer runs are read again
 constexpr int kMaxCluster = 8;
 constexpr int kMove = 8;                       // rows in flight per thread
 
@@ -50,13 +50,14 @@ __device__ __forceinline__ int checked_len(const EvictArgs& a, int s) {
   return min(len, a.num_keep) > a.max_kept ? -1 : len;
 }
 
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 2)
     evict_kernel(const __grid_constant__ EvictArgs a) {
   constexpr uint32_t FULL = 0xffffffffu;
   __shared__ __align__(8) uint32_t keys[kKeys];
-  __shared__ uint32_t hist[2][256];            // digit counts of this CTA, by pass parity
-  __shared__ uint32_t total[256];              // of the cluster
-  __shared__ uint32_t pick[2];                 // digit, how many to take inside it
+  // Digit counts of this CTA, the highest digit first.  Three in turn: pass p fills one and clears the next, which
+  // was last read in pass p - 2, so before everybody came to pass p - 1's barrier.
+  __shared__ __align__(16) uint32_t hist[3][256];
+  __shared__ __align__(16) uint32_t total[256];   // of the cluster
   __shared__ uint32_t counts[2];               // this CTA's keys above / equal to the threshold
   __shared__ uint32_t wcount[2][kWarps];
   cg::cluster_group cluster = cg::this_cluster();
@@ -80,9 +81,13 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int m = min(len, a.num_keep);
   const int old = max(0, len - a.num_recent);  // tokens that compete by score
   const int r = m - (len - old);               // how many of them stay
+  auto sync = [&]() {
+    if (nc > 1) cluster.sync();
+    else __syncthreads();
+  };
   auto put = [&](int place, int t) {
+    if (place >= m) return;                    // scores that change meanwhile stay harmless
     kept[place] = t;
-    if (nsc) nsc[place] = sc[t];
   };
   if (r > 0 && r < old) {
     // this CTA's run of tokens, in whole warps of 32 for each of its warps
@@ -93,53 +98,64 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (held)
       for (int t = t_lo + tid; t < t_hi; t += kThreads) keys[t - t_lo] = score_key(sc[t]);
     auto key = [&](int t) { return held ? keys[t - t_lo] : score_key(sc[t]); };
+    if (tid < 256) hist[0][tid] = 0;
+    __syncthreads();
     uint32_t thr = 0, mask = 0, want = static_cast<uint32_t>(r);
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass, buf = pass & 1;
-      if (tid < 256) hist[buf][tid] = 0;
-      __syncthreads();
-      for (int t = t_lo + tid; t < t_hi; t += kThreads) {
-        const uint32_t k = key(t);
-        if ((k & mask) == thr) atomicAdd(&hist[buf][(k >> shift) & 255u], 1u);
-      }
-      cluster.sync();
-      if (tid < 256) {
-        uint32_t sum = 0;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          if (c < nc) sum += cluster.map_shared_rank(&hist[buf][0], c)[tid];
-        total[tid] = sum;
-      }
-      __syncthreads();
-      if (warp == 0) {                         // lane l: digits 255 - 8l .. 248 - 8l
-        uint32_t c[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          c[i] = total[255 - 8 * lane - i];
-          sum += c[i];
+      const int shift = 24 - 8 * pass, buf = pass % 3;
+      if (tid < 256) hist[(pass + 1) % 3][tid] = 0;
+      if (pass == 0) {
+        // sign and exponent: a warp's keys share a few digits, so equal ones are counted
+        // by one lane (32 lanes on one counter take 32 turns)
+        for (int t = t_lo + tid; t < t_hi; t += kThreads) {
+          const uint32_t d = 255u - (key(t) >> 24);
+          const uint32_t same = __match_any_sync(__activemask(), d);
+          if (lane == __ffs(same) - 1) atomicAdd(&hist[0][d], __popc(same));
         }
-        uint32_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_up_sync(FULL, incl, o);
-          if (lane >= o) incl += v;
-        }
-        uint32_t before = incl - sum;
-        if (before < want && incl >= want) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (before < want && before + c[i] >= want) {
-              pick[0] = 255 - 8 * lane - i;
-              pick[1] = want - before;
-            }
-            before += c[i];
-          }
+      } else {
+        for (int t = t_lo + tid; t < t_hi; t += kThreads) {
+          const uint32_t k = key(t);
+          if ((k & mask) == thr) atomicAdd(&hist[buf][255u - ((k >> shift) & 255u)], 1u);
         }
       }
-      __syncthreads();
-      thr |= pick[0] << shift;
-      want = pick[1];
+      sync();
+      const uint32_t* sum_of = hist[buf];
+      if (nc > 1) {
+        if (tid < 256) {
+          uint32_t sum = 0;
+#pragma unroll
+          for (int c = 0; c < kMaxCluster; ++c)
+            if (c < nc) sum += cluster.map_shared_rank(&hist[buf][0], c)[tid];
+          total[tid] = sum;
+        }
+        __syncthreads();
+        sum_of = total;
+      }
+      // every warp finds the digit for itself; lane l: digits 255 - 8l .. 248 - 8l
+      const uint4 c0 = reinterpret_cast<const uint4*>(sum_of)[2 * lane];
+      const uint4 c1 = reinterpret_cast<const uint4*>(sum_of)[2 * lane + 1];
+      const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+      const uint32_t sum = c0.x + c0.y + c0.z + c0.w + c1.x + c1.y + c1.z + c1.w;
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(FULL, incl, o);
+        if (lane >= o) incl += v;
+      }
+      uint32_t before = incl - sum, digit = 0, inside = 0;
+      const bool mine = before < want && incl >= want;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (mine && before < want && before + c[i] >= want) {
+          digit = 255 - 8 * lane - i;
+          inside = want - before;
+        }
+        before += c[i];
+      }
+      const int src = __ffs(__ballot_sync(FULL, mine)) - 1;
+      thr |= __shfl_sync(FULL, digit, src) << shift;
+      want = __shfl_sync(FULL, inside, src);
       mask |= 255u << shift;
     }
     // `want` of the tokens equal to the threshold stay, the first ones
@@ -161,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       for (int w = 0; w < kWarps; ++w) sum += wcount[tid][w];
       counts[tid] = sum;
     }
-    cluster.sync();
+    sync();
     above = equal = 0;                         // before this warp's first token
     for (int c = 0; c < rank; ++c) {
       const uint32_t* other = cluster.map_shared_rank(&counts[0], c);
@@ -193,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (tid == 0 && kvh == 0 && rank == 0) a.new_lens[s] = m;
   // every place is written (the barrier orders the cluster's global writes too), and
   // nobody reads this CTA's shared memory any more
-  cluster.sync();
+  sync();
 
   // ---- copy the kept rows: this CTA takes a run of places; their source and destination
   // slots go to shared memory first (in place of the keys), so that a row's copy waits
@@ -215,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     for (int i = tid; i < n; i += kThreads) {
       const int j = base + i, t = __ldcg(kept + j);
       const int sb = stab[t >> bsh], db = dtab[j >> bsh];
+      if (nsc) nsc[j] = sc[t];
       const bool ok = sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks;
       const int from = (sb << bsh) + (t & bmask), to = (db << bsh) + (j & bmask);
       if (!ok) report_error(a.err_flag, kErrBlockId);      // not copied
@@ -256,12 +273,13 @@ cudaError_t launch_evict(const EvictArgs& a0, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  // CTAs per (sequence, kv head): until four fill an SM, while each has 256 tokens to look at
+  // CTAs per (sequence, kv head): until every SM has one, while each has 1024 tokens to
+  // look at (a cluster's barriers and remote reads cost ~1 us a digit)
   const long long cap = static_cast<long long>(a.max_src_blocks) * a.block_size;
   const long long width = cap < a.score_stride ? cap : a.score_stride;
   const long long units = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
   unsigned nc = 1;
-  while (nc < kMaxCluster && units * nc < 4LL * sms && width >= 512LL * nc) nc *= 2;
+  while (nc < kMaxCluster && units * nc < sms && width >= 2048LL * nc) nc *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nc, a.num_kv_heads, a.num_seqs);
   cfg.blockDim = dim3(kThreads);
