@@ -31,6 +31,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
+// Bound: the rows' bytes, each read and written once.  8191 tokens x 80 rows x 128 bf16
+// (336 MB): 61.4 us, 5.5 TB/s.  Two or three rows' loads in flight per lane, or the first
+// ones before the sine and cosine, were slower (63 to 83 us: fewer CTAs fit an SM).
 // One CTA per (token, slice of its rows).  A row of D elements is D / (2 VE) lanes'
 // work; lane j of a row holds pairs [j VE, (j + 1) VE): its two 16-byte vectors are the
 // halves' vectors j (halves form) or the row's vectors 2j and 2j + 1 (side by side).
@@ -162,8 +165,17 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename ST, int MODE, int D>
 cudaError_t launch_t(const RopeArgs& a, cudaStream_t s) {
-  return launch_kernel(rope_kernel<ST, MODE, D>, dim3(a.num_tokens, 1), dim3(kThreads), 0, s,
-                       pdl_mode() != 0, a);
+  // few tokens: a token's rows over several CTAs, until every SM has one (32 tokens of
+  // 80 rows: 2.4 us against 3.8 with a CTA each)
+  constexpr int kRowsPerPass = kThreads / (D / (32 / static_cast<int>(sizeof(ST))));
+  const long long passes = (a.num_heads + 2LL * a.num_kv_heads + kRowsPerPass - 1) / kRowsPerPass;
+  int sms = 0;
+  const cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  long long slices = (sms + a.num_tokens - 1) / a.num_tokens;
+  if (slices > passes) slices = passes;
+  return launch_kernel(rope_kernel<ST, MODE, D>, dim3(a.num_tokens, static_cast<unsigned>(slices)),
+                       dim3(kThreads), 0, s, pdl_mode() != 0, a);
 }
 
 template <typename ST>
