@@ -23,7 +23,7 @@ cudaError_t launch_t(const PrefillArgs& a, int total_q, int max_query_len, cudaS
   const int rows_per_cta = kQTiles * (kRows / G);
   const dim3 grid((max_query_len + rows_per_cta - 1) / rows_per_cta, a.num_kv_heads,
                   a.cascade_rows > 0 ? max(1, a.cascade_splits) : a.num_seqs);
-  return launch_kernel(kern, grid, dim3(prefill_threads<-1>()), kSmemBytes, stream,
+  return launch_kernel(kern, grid, dim3(kThreads), kSmemBytes, stream,
                        allow_pdl && pdl_mode() != 0, mq, mk, mv, a);
 }
 

@@ -89,11 +89,12 @@ constexpr int kKOff = kQTiles * 2 * kQHalf;
 constexpr int kVOff = kKOff + kKst * kKvTile;
 constexpr int kSmemBytes = kVOff + kVst * kKvTile + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;        // S_A, S_B, O_A, O_B: 128 columns each
-// Softmax warps: one thread per row (8 warps), or two with MOD >= 0 (16 warps).
-template <int MOD>
-__host__ __device__ constexpr int softmax_warps() { return MOD >= 0 ? 16 : 8; }
-template <int MOD>
-__host__ __device__ constexpr int prefill_threads() { return 32 * (softmax_warps<MOD>() + 2); }
+constexpr int kThreads = 320;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+// MOD >= 0: the KV tiles' two 64-token halves are steps of their own, with S and P apart
+// in TMEM (S_A, S_B, P_A, P_B: 64 columns each, O_A, O_B: 128), so that the next step's S
+// can be computed while this one's softmax runs.
+constexpr int kSub = 64;
 
 // bf16 keeps 8 significant bits: P goes in as a high and a low bf16 part (two
 // PV products, ~16 bits); fp16's 11 bits need one.  P of 128 tokens takes 64
@@ -101,12 +102,6 @@ __host__ __device__ constexpr int prefill_threads() { return 32 * (softmax_warps
 template <typename QT, int MOD>
 __host__ __device__ constexpr int p_parts() {
   return MOD >= 0 || std::is_same<QT, __nv_bfloat16>::value ? 2 : 1;
-}
-
-// MOD >= 0: TMEM column (from S) of the P operand of tokens [16 kk, 16 kk + 16): the
-// 32-column chunk of 32 tokens holds 16 columns of high parts, then 16 of low parts.
-__device__ __forceinline__ uint32_t mask_p_col(int part, int kk) {
-  return static_cast<uint32_t>((kk >> 1) * 32 + part * 16 + (kk & 1) * 8);
 }
 
 // ---- packed f32x2 arithmetic: two FP32 results per instruction
@@ -158,8 +153,8 @@ enum {
   kBarQ = 0, kBarKFull = 1, kBarKEmpty = kBarKFull + kKst, kBarVFull = kBarKEmpty + kKst,
   kBarVEmpty = kBarVFull + kVst, kBarSFull = kBarVEmpty + kVst, kBarPFull = kBarSFull + 2,
   kBarODone = kBarPFull + 2, kBarDrain = kBarODone + 2,
-  kBarPair = kBarDrain + 1,                  // MOD >= 0: a row's two threads (8 warp pairs)
-  kNumBars = kBarPair + 8
+  kBarSFree = kBarDrain + 1,                 // MOD >= 0: S is in the softmax's registers
+  kNumBars = kBarSFree + 2
 };
 
 // MOD >= 0: y -> factor * tanh(y) for |y| <= 1, as factor * y * Q(y^2): Q of degree 5
@@ -235,7 +230,7 @@ __device__ __noinline__ void masked_row(const PrefillArgs& a, const int32_t* tab
 
 // BSC: tokens per block, 0: a.block_size.
 template <typename QT, int BSC, int MOD = -1>
-__global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PrefillArgs a) {
   constexpr bool MASK = MOD >= 0, CAP = MASK && (MOD & 1), BIAS = MASK && (MOD & 2);
@@ -244,21 +239,12 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
   const int NBOX = kBN / BOXH;             // boxes per 64-column half
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
   constexpr int PARTS = p_parts<QT, MOD>();
-  constexpr int NSM = softmax_warps<MOD>();
-  constexpr int TW = NSM / 2;                // softmax warps per query tile
-  constexpr int HALVES = TW / 4;             // threads per row
-  constexpr int kTmaWarp = NSM, kMmaWarp = NSM + 1;
   constexpr uint32_t FULL = 0xffffffffu;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
-  __shared__ int span_lo[NSM], span_hi[NSM];  // MASK: the union of each softmax warp's spans
-  // MASK: each softmax thread's maximum for the row's other thread (whole log2 units;
-  // kNone: no seen token).  One buffer: a thread writes step j + 1's only after S(j + 1),
-  // so after both threads of the row have handed over P(j), having read step j's.
-  constexpr int kNone = -32768;
-  __shared__ int16_t pair_max[MASK ? 512 : 1];
+  __shared__ int span_lo[8], span_hi[8];     // MASK: the union of each softmax warp's spans
 
   const int tile2 = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -290,8 +276,8 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
   // MASK: this thread's row and the tokens it sees; the union of the CTA's rows
   int row_lo = 0, row_hi = 0, row_pos = -1, u_lo = 0, u_hi = 0;
   if constexpr (MASK) {
-    if (warp < NSM) {
-      const int r = (tid % kRows) / G, tok = row0 + (warp / TW) * TQ + r;
+    if (warp < 8) {
+      const int r = (tid % kRows) / G, tok = row0 + (warp / 4) * TQ + r;
       if (r < TQ && tok < q_len) {
         row_pos = L - q_len + tok;
         const Span sp = seen_span(a.kv_start ? a.kv_start[q0 + tok] : 0, row_pos, a.window,
@@ -326,8 +312,8 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool from_threads = i >= kBarPFull && i < kBarPFull + 2;
-      mbar_init(bar(i), from_threads ? kRows * HALVES : (i >= kBarPair ? 64 : 1));
+      const bool from_threads = (i >= kBarPFull && i < kBarPFull + 2) || i >= kBarSFree;
+      mbar_init(bar(i), from_threads ? kRows : 1);
     }
     abort_flag = 0;
     fence_barrier_init();
@@ -346,25 +332,28 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
   if constexpr (MASK) {
     u_lo = span_lo[0];
     u_hi = span_hi[0];
-    for (int w = 1; w < NSM; ++w) {
+    for (int w = 1; w < 8; ++w) {
       u_lo = min(u_lo, span_lo[w]);
       u_hi = max(u_hi, span_hi[w]);
     }
     t_lo = u_lo < u_hi ? u_lo / kBN : 0;
     ntiles = u_lo < u_hi ? (u_hi - 1) / kBN + 1 - t_lo : 0;
   }
+  // MASK: steps [i0, i1) of 64 tokens, counted from the first KV tile
+  const int i0 = MASK ? u_lo / kSub - t_lo * (kBN / kSub) : 0;
+  const int i1 = MASK && ntiles > 0 ? (u_hi - 1) / kSub + 1 - t_lo * (kBN / kSub) : i0;
   // S_x (f32) and, over it once read, P_x (16-bit pairs per column; bf16's low
   // part in columns 64..127)
-  auto t_s = [&](int x) { return tmem + static_cast<uint32_t>(128 * x); };
+  auto t_s = [&](int x) { return tmem + static_cast<uint32_t>((MASK ? kSub : 128) * x); };
+  auto t_p = [&](int x) { return tmem + static_cast<uint32_t>(2 * kSub + kSub * x); };   // MASK
   auto t_o = [&](int x) { return tmem + 256u + static_cast<uint32_t>(128 * x); };
 
-  // softmax state, kept here for the epilogue
-  const int x_me = warp < NSM ? warp / TW : 0;
-  const int half_me = MASK && warp < NSM ? (warp / 4) % HALVES : 0;
+  // softmax state (warps 0-7), kept here for the epilogue
+  const int x_me = warp < 8 ? warp / 4 : 0;
   const int row_me = tid % kRows;
   const int r_tok = row_me / G;
   const int tok_me = row0 + x_me * TQ + r_tok;          // query token within the chunk
-  const bool row_valid = warp < NSM && tok_me < q_len && (!MASK || r_tok < TQ);
+  const bool row_valid = warp < 8 && tok_me < q_len && (!MASK || r_tok < TQ);
   float m_run = -INFINITY, l_run = 0.f;
   int armed_k[kKst], armed_v[kVst];          // TMA warp: last tile issued into each stage
 #pragma unroll
@@ -471,14 +460,81 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
       for (int part = 0; part < PARTS; ++part) {
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_f16_ts_warp(t_o(x), t_s(x) + (MASK ? mask_p_col(part, kk)
-                                                  : static_cast<uint32_t>(part * 64 + kk * 8)),
+          umma_f16_ts_warp(t_o(x), t_s(x) + static_cast<uint32_t>(part * 64 + kk * 8),
                            vd + static_cast<uint32_t>(kk * 16 * 128 >> 4), idesc_o,
                            j > 0 || part > 0 || kk > 0);
       }
       umma_commit_warp(bar(kBarODone + x));
     };
-    bool ok = wait1(kBarQ, 0);
+    if constexpr (MASK) {
+      const uint32_t idesc_s64 = umma_idesc_f16(kBf16, false, kRows, kSub);
+      auto sub_s = [&](int x, int i) {       // S_x = Q_x K^T over step i's 64 tokens
+        tc_fence_after_sync();
+        const uint64_t qd = dq0 + static_cast<uint64_t>(x * (2 * kQHalf >> 4));
+        const uint64_t kd = dk0 + static_cast<uint64_t>((((i >> 1) % kKst) * kKvTile +
+                                                         (i & 1) * kSub * 128) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t qoff = static_cast<uint32_t>(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4);
+          const uint32_t koff = static_cast<uint32_t>(((kk >> 2) * kKvHalf + (kk & 3) * 32) >> 4);
+          umma_f16_ss_warp(t_s(x), qd + qoff, kd + koff, idesc_s64, kk > 0);
+        }
+        umma_commit_warp(bar(kBarSFull + x));
+      };
+      auto sub_pv = [&](int x, int i) {      // O_x += P_x V: high parts, then low parts
+        tc_fence_after_sync();
+        const uint64_t vd = dv0 + static_cast<uint64_t>((((i >> 1) % kVst) * kKvTile +
+                                                         (i & 1) * kSub * 128) >> 4);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+#pragma unroll
+          for (int kk = 0; kk < kSub / 16; ++kk)
+            umma_f16_ts_warp(t_o(x), t_p(x) + static_cast<uint32_t>(part * 32 + kk * 8),
+                             vd + static_cast<uint32_t>(kk * 16 * 128 >> 4), idesc_o,
+                             i > i0 || part > 0 || kk > 0);
+        }
+        umma_commit_warp(bar(kBarODone + x));
+      };
+      bool ok = wait1(kBarQ, 0);
+      if (ok && i0 < i1) ok = wait1(kBarKFull, 0);
+      if (ok && i0 < i1) {
+        sub_s(0, i0);
+        sub_s(1, i0);
+        if ((i0 & 1) || i0 + 1 == i1) umma_commit_warp(bar(kBarKEmpty));
+      }
+      for (int i = i0; ok && i < i1; ++i) {
+        const int j = i >> 1, vs = j % kVst, n = i - i0;
+        if (i + 1 < i1) {                    // the next step's S, once this one's is read
+          const int jn = (i + 1) >> 1;
+          if (jn != j && !(ok = wait1(kBarKFull + jn % kKst, (jn / kKst) & 1))) break;
+          if (!(ok = wait1(kBarSFree + 0, n & 1))) break;
+          sub_s(0, i + 1);
+          if (!(ok = wait1(kBarSFree + 1, n & 1))) break;
+          sub_s(1, i + 1);
+          if (((i + 1) & 1) || i + 2 == i1) umma_commit_warp(bar(kBarKEmpty + jn % kKst));
+        }
+        if (i == i0 || !(i & 1)) {           // the tile's V, at its first step
+          if (!(ok = wait1(kBarVFull + vs, (j / kVst) & 1))) break;
+          const int first = max(0, u_lo - (t_lo + j) * kBN), last = min(kBN, u_hi - (t_lo + j) * kBN);
+          if (first > 0 || last < kBN) {     // rows that no row of the CTA sees: zeros
+            for (int idx = lane; idx < kBN * 16; idx += 32) {
+              const int row = idx / 16, ch = idx % 16;
+              if (row >= first && row < last) continue;
+              const uint32_t addr = v_s(vs) + (ch >> 3) * kKvHalf + row * 128 + (ch & 7) * 16;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (!(ok = wait1(kBarPFull + 0, n & 1))) break;
+        sub_pv(0, i);
+        if (!(ok = wait1(kBarPFull + 1, n & 1))) break;
+        sub_pv(1, i);
+        if ((i & 1) || i + 1 == i1) umma_commit_warp(bar(kBarVEmpty + vs));
+      }
+    }
+    bool ok = !MASK && wait1(kBarQ, 0);
     if (ok && ntiles > 0) {
       ok = wait1(kBarKFull, 0);
       if (ok) {
@@ -490,19 +546,7 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
     for (int j = 0; ok && j < ntiles; ++j) {
       const int vs = j % kVst;
       if (!(ok = wait1(kBarVFull + vs, (j / kVst) & 1))) break;
-      if (MASK && ((t_lo + j) * kBN < u_lo || (t_lo + j) * kBN + kBN > u_hi)) {
-        // V rows that no row of the CTA sees (past the sequence's end among them)
-        const int first = max(0, u_lo - (t_lo + j) * kBN), last = min(kBN, u_hi - (t_lo + j) * kBN);
-        for (int idx = lane; idx < kBN * 16; idx += 32) {
-          const int row = idx / 16, ch = idx % 16;
-          if (row >= first && row < last) continue;
-          const uint32_t addr = v_s(vs) + (ch >> 3) * kKvHalf + row * 128 + (ch & 7) * 16;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (!MASK && (t_lo + j) * kBN + kBN > L) {
+      if ((t_lo + j) * kBN + kBN > L) {
         // V rows at or past the sequence end: zero them so that poisoned or
         // stale slots cannot turn 0 * x into NaN inside the MMA
         const int first = max(0, L - (t_lo + j) * kBN);
@@ -538,149 +582,139 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
     float slope = 0.f;
     if (BIAS && row_valid) slope = a.slopes[kvh * G + row_me % G] * kLog2e;
     if constexpr (MASK) {
-      // Two threads per row, columns [64 half, 64 half + 64): scores in registers, the
-      // row's maximum exchanged, P over the columns each thread has read (a 32-column
-      // chunk holds its tokens' 16 columns of high parts, then 16 of low parts).
-      constexpr int NC = kBN / HALVES;       // columns per thread
-      const int pair = x * 4 + (warp & 3);
-      const int mine = (x * 2 + half_me) * kRows + row_me, other = (x * 2 + 1 - half_me) * kRows + row_me;
-      const uint32_t s_col = t_s(x) + lane_off + static_cast<uint32_t>(half_me * NC);
-      for (int j = 0; j < ntiles; ++j) {
-        if (!mbar_wait_abortable(bar(kBarSFull + x), j & 1, a.timeout_ns, abort)) break;
+      constexpr int NC = kSub;
+      for (int i = i0; i < i1; ++i) {
+        const int n = i - i0;
+        if (!mbar_wait_abortable(bar(kBarSFull + x), n & 1, a.timeout_ns, abort)) break;
         tc_fence_after_sync();
         float sv[NC];
 #pragma unroll
-        for (int i = 0; i < NC / 32; ++i) {
+        for (int q = 0; q < NC / 32; ++q) {
           float v[32];
-          tmem_ld32(s_col + 32 * i, v);
+          tmem_ld32(t_s(x) + lane_off + 32 * q, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[32 * i + e] = v[e];
+          for (int e = 0; e < 32; ++e) sv[32 * q + e] = v[e];
         }
         tmem_wait_ld();
-        const int t_base = (t_lo + j) * kBN + half_me * NC;  // the token of column 0
-        const bool off = row_lo >= row_hi;   // this row sees nothing
+        tc_fence_before_sync();
+        mbar_arrive(bar(kBarSFree + x));     // the next step's S may come
+
+        const int t_base = t_lo * kBN + i * kSub;            // the token of column 0
         // every column seen by every row of the warp; else a bit per seen column (a test
         // of two bounds per element would cost as much as the rest of the softmax)
+        const bool off = row_lo >= row_hi;   // this row sees nothing
         const bool full = __all_sync(FULL, !row_valid || (row_lo <= t_base && row_hi >= t_base + NC));
         uint32_t bits[NC / 32];
 #pragma unroll
-        for (int i = 0; i < NC / 32; ++i) {
-          const int from = max(0, min(32, row_lo - t_base - 32 * i));
-          const int to = max(0, min(32, row_hi - t_base - 32 * i));
-          bits[i] = from < to ? (FULL >> (32 - (to - from))) << from : 0u;
+        for (int q = 0; q < NC / 32; ++q) {
+          const int from = max(0, min(32, row_lo - t_base - 32 * q));
+          const int to = max(0, min(32, row_hi - t_base - 32 * q));
+          bits[q] = from < to ? (FULL >> (32 - (to - from))) << from : 0u;
         }
         auto seen = [&](int c) { return ((bits[c / 32] >> (c % 32)) & 1u) != 0; };
 
-        // The usual tile: the cap as a polynomial (every |score| within the cap's unit
-        // range), the bias linear in the column (all of the tile on one side of pos).
-        // Else the scores are changed element by element.
-        const int d0 = t_base - row_pos;     // column c is at distance |c + d0|
-        bool usual = true;
+        // The scores.  The cap as a polynomial where every |score| of the warp is within its
+        // unit range (it grows with the score, so the maximum can be taken before it and
+        // the polynomial left to the pass that makes P), else tanh over its whole range; the
+        // bias by packed adds where all of the step is on one side of pos.
+        float factor = a.scale_log2;         // what turns sv into scores in log2 units
+        bool poly = false;
         if constexpr (CAP) {
           float big[2] = {0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < NC; c += 2)
             big[(c >> 1) & 1] = fmax3_abs(big[(c >> 1) & 1], sv[c], sv[c + 1]);
-          usual = off || fmaxf(big[0], big[1]) * fabsf(a.cap_in) <= 1.f;
-        }
-        bool before = true;
-        if constexpr (BIAS) {
-          before = d0 + NC - 1 <= 0;
-          usual = usual && (off || before || d0 >= 0);
-        }
-        usual = (!CAP && !BIAS) || __all_sync(FULL, usual);
-        // one score of an unusual tile, in log2 units (column c)
-        auto score = [&](float v, int c) {
-          float y = CAP ? a.cap_log2 * tanh_f32(v * a.cap_in) : v * a.scale_log2;
-          if constexpr (BIAS) y = fmaf(-slope, fabsf(static_cast<float>(d0 + c)), y);
-          return y;
-        };
-
-        // The row's maximum, or in the usual tile what the cap makes of the largest product
-        // with no bias (which only lowers it): enough to tell whether the base has to move.
-        float mx[2] = {-INFINITY, -INFINITY}, top;
-        if (usual) {
-          const float dir = CAP ? a.cap_in : a.scale_log2;
-          if (full && dir >= 0.f) {
+          poly = __all_sync(FULL, off || fmaxf(big[0], big[1]) * fabsf(a.cap_in) <= 1.f);
+          factor = a.cap_in;
+          if (!poly) {
 #pragma unroll
-            for (int c = 0; c < NC; c += 2)
-              mx[(c >> 1) & 1] = fmax3(mx[(c >> 1) & 1], sv[c], sv[c + 1]);
-          } else {
-            const float sg = dir >= 0.f ? 1.f : -1.f;    // (bits cover a whole tile too)
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-              mx[c & 1] = fmaxf(mx[c & 1], seen(c) ? sg * sv[c] : -INFINITY);
+            for (int c = 0; c < NC; ++c) sv[c] = a.cap_log2 * tanh_f32(sv[c] * a.cap_in);
+            factor = 1.f;
           }
-          top = fmaxf(mx[0], mx[1]);
-          if (top != -INFINITY)
-            top = CAP ? a.cap_log2 * tanh_f32(top * fabsf(a.cap_in)) : top * fabsf(a.scale_log2);
+        }
+        if constexpr (BIAS) {
+          const int d0 = t_base - row_pos;   // column c is at distance |c + d0|
+          const bool before = d0 + NC - 1 <= 0;
+          if (__all_sync(FULL, off || before) || __all_sync(FULL, off || d0 >= 0)) {
+            const CapPoly<QT> cap(a.cap_log2);
+            const uint64_t f2 = f2splat(factor);
+            const float sg = before ? slope : -slope;
+            const uint64_t step = f2splat(2.f * sg);
+#pragma unroll
+            for (int c32 = 0; c32 < NC; c32 += 32) {
+              const float b0 = sg * static_cast<float>(d0 + c32);
+              uint64_t b = f2pack(b0, b0 + sg);
+              if (CAP && poly) {
+#pragma unroll
+                for (int c = c32; c < c32 + 32; c += 2) {
+                  const float2 y = f2unpack(cap(f2mul(f2pack(sv[c], sv[c + 1]), f2), b));
+                  sv[c] = y.x;
+                  sv[c + 1] = y.y;
+                  b = f2add(b, step);
+                }
+              } else {
+#pragma unroll
+                for (int c = c32; c < c32 + 32; c += 2) {
+                  const float2 y = f2unpack(f2fma(f2pack(sv[c], sv[c + 1]), f2, b));
+                  sv[c] = y.x;
+                  sv[c + 1] = y.y;
+                  b = f2add(b, step);
+                }
+              }
+            }
+          } else {
+            const float d = static_cast<float>(d0);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const float y = CAP && poly ? a.cap_log2 * tanh_f32(sv[c] * factor) : sv[c] * factor;
+              sv[c] = fmaf(-slope, fabsf(d + static_cast<float>(c)), y);
+            }
+          }
+          poly = false;
+          factor = 1.f;
+        }
+
+        float mx[2] = {-INFINITY, -INFINITY};
+        if (full && factor >= 0.f) {
+#pragma unroll
+          for (int c = 0; c < NC; c += 2)
+            mx[(c >> 1) & 1] = fmax3(mx[(c >> 1) & 1], sv[c], sv[c + 1]);
         } else {
+          const float sg = factor >= 0.f ? 1.f : -1.f;       // (bits cover a whole step too)
 #pragma unroll
           for (int c = 0; c < NC; ++c)
-            mx[c & 1] = fmaxf(mx[c & 1], seen(c) ? score(sv[c], c) : -INFINITY);
-          top = fmaxf(mx[0], mx[1]);
+            mx[c & 1] = fmaxf(mx[c & 1], seen(c) ? sg * sv[c] : -INFINITY);
         }
-        // the exponent base is a whole number at or above the row's maximum, moved only
-        // when that exceeds it by more than 8.  A maximum past +-32767 ends in a row
-        // without a finite positive sum, which is computed again below.
-        const int top_i = top == -INFINITY ? kNone : max(-32767, min(32767, __float2int_ru(top)));
-        pair_max[mine] = static_cast<int16_t>(top_i);
-        mbar_arrive(bar(kBarPair + pair));
+        const float rmax = fmaxf(mx[0], mx[1]);
+        float tmax = rmax;
+        if (rmax != -INFINITY) {
+          tmax = rmax * fabsf(factor);
+          if (CAP && poly) tmax = a.cap_log2 * tanh_f32(tmax);
+        }
+        // the exponent base moves only when the step's maximum exceeds it by more than 8
+        const float m_new = tmax > m_run + 8.f ? tmax : m_run;
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = m_new == m_run ? 1.f : fast_exp2(m_run - base);
+        m_run = m_new;
 
-        // With no maximum of its own past the base, a warp goes on at the base as it
-        // stands while the row's other thread gets to its maximum; should that move the
-        // base, P is scaled afterwards (by a power of two: the base is whole).
-        auto wait_pair = [&]() {
-          return mbar_wait_abortable(bar(kBarPair + pair), j & 1, a.timeout_ns, abort);
-        };
-        float alpha = 1.f;                   // what a move of the base makes of l and O
-        auto move_base = [&]() {
-          const int both = max(top_i, static_cast<int>(pair_max[other]));
-          const float tmax = both == kNone ? -INFINITY : static_cast<float>(both);
-          if (tmax > m_run + 8.f) {
-            alpha = fast_exp2(m_run - tmax);
-            m_run = tmax;
-          }
-        };
-        const bool first = __any_sync(FULL, !off && (m_run == -INFINITY || (top_i != kNone &&
-                                            static_cast<float>(top_i) > m_run + 8.f)));
-        if (first) {
-          if (!wait_pair()) break;
-          move_base();
-        }
+        // P and O are free to be written once the last step's PV is done
+        if (n > 0 && !mbar_wait_abortable(bar(kBarODone + x), (n - 1) & 1, a.timeout_ns, abort)) break;
+        tc_fence_after_sync();
         uint64_t ps2[2];
-        auto emit = [&](auto poly, auto whole, float base) {
-          constexpr bool POLY = decltype(poly)::value;       // a usual tile
+        auto emit = [&](auto cap_now, auto whole) {
+          constexpr bool POLY = decltype(cap_now)::value;    // the cap is still to be taken
           constexpr bool WHOLE = decltype(whole)::value;     // every column is seen
           const CapPoly<QT> cap(a.cap_log2);
-          const uint64_t sc2 = f2splat(CAP ? a.cap_in : a.scale_log2), nb2 = f2splat(-base);
-          const float sg = before ? slope : -slope;
+          const uint64_t sc2 = f2splat(factor), nb2 = f2splat(-base);
           ps2[0] = ps2[1] = f2splat(0.f);
 #pragma unroll
-          for (int c32 = 0; c32 < NC / 32; ++c32) {
-            // the products once more: kept from the first pass, they and the 32 words of P
-            // would not fit 96 registers
-            float sv[32];
-            tmem_ld32(s_col + 32 * c32, sv);
-            tmem_wait_ld();
+          for (int q = 0; q < NC / 32; ++q) {
             uint32_t hw[16], lw[16];
-            uint64_t b = nb2;
-            const uint64_t step = f2splat(2.f * sg);
-            if constexpr (BIAS && POLY) {
-              const float b0 = sg * static_cast<float>(d0 + 32 * c32);
-              b = f2add(f2pack(b0, b0 + sg), nb2);
-            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int c = 32 * c32 + 2 * e;
-              const uint64_t s2 = f2pack(sv[2 * e], sv[2 * e + 1]);
-              float2 xx;
-              if constexpr (POLY) {
-                xx = f2unpack(CAP ? cap(f2mul(s2, sc2), b) : f2fma(s2, sc2, b));
-                if constexpr (BIAS) b = f2add(b, step);
-              } else {
-                xx = make_float2(score(sv[2 * e], c) - base, score(sv[2 * e + 1], c + 1) - base);
-              }
+              const int c = 32 * q + 2 * e;
+              const uint64_t s2 = f2pack(sv[c], sv[c + 1]);
+              const float2 xx = f2unpack(POLY ? cap(f2mul(s2, sc2), nb2) : f2fma(s2, sc2, nb2));
               float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
               if constexpr (!WHOLE) {
                 p.x = seen(c) ? p.x : 0.f;
@@ -693,60 +727,33 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
               const float2 rest = f2unpack(f2sub(p2, f2pack(f.x, f.y)));
               lw[e] = pack2<QT>(rest.x, rest.y);
             }
-            tmem_st16(s_col + 32 * c32, hw);
-            tmem_st16(s_col + 32 * c32 + 16, lw);
+            tmem_st16(t_p(x) + lane_off + 16 * q, hw);
+            tmem_st16(t_p(x) + lane_off + 32 + 16 * q, lw);
           }
         };
-        const float base = m_run == -INFINITY ? 0.f : m_run;
         using Yes = std::true_type;
         using No = std::false_type;
-        if (usual) full ? emit(Yes{}, Yes{}, base) : emit(Yes{}, No{}, base);
-        else emit(No{}, No{}, base);
+        if (CAP && poly) full ? emit(Yes{}, Yes{}) : emit(Yes{}, No{});
+        else full ? emit(No{}, Yes{}) : emit(No{}, No{});
         const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
-        float sum = (s0.x + s0.y) + (s1.x + s1.y);
-        if (!first) {
-          if (!wait_pair()) break;
-          move_base();
-          if (__any_sync(FULL, alpha != 1.f)) {
-            sum *= alpha;
-            tmem_wait_st();
-#pragma unroll 1
-            for (int c32 = 0; c32 < NC / 32; ++c32) {
-              float v[32];
-              tmem_ld32(s_col + 32 * c32, v);
-              tmem_wait_ld();
-              uint32_t hw[16], lw[16];
+        l_run = l_run * alpha + ((s0.x + s0.y) + (s1.x + s1.y));
+        if (n > 0 && __any_sync(FULL, alpha != 1.f)) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 h = unpack2<QT>(__float_as_uint(v[e]));
-                const float2 l = unpack2<QT>(__float_as_uint(v[16 + e]));
-                const float2 p = make_float2((h.x + l.x) * alpha, (h.y + l.y) * alpha);
-                hw[e] = pack2<QT>(p.x, p.y);
-                const float2 f = unpack2<QT>(hw[e]);
-                lw[e] = pack2<QT>(p.x - f.x, p.y - f.y);
-              }
-              tmem_st16(s_col + 32 * c32, hw);
-              tmem_st16(s_col + 32 * c32 + 16, lw);
-            }
-          }
-        }
-        l_run = l_run * alpha + sum;
-        if (j > 0 && __any_sync(FULL, alpha != 1.f)) {       // each thread half of the row's O
-#pragma unroll
-          for (int i = 0; i < 4 / HALVES; ++i) {
-            const uint32_t o_col = t_o(x) + lane_off + static_cast<uint32_t>(half_me * 64 + 32 * i);
+          for (int q = 0; q < 4; ++q) {
             float v[32];
-            tmem_ld32(o_col, v);
+            tmem_ld32(t_o(x) + lane_off + 32 * q, v);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] *= alpha;
-            tmem_st32(o_col, v);
+            tmem_st32(t_o(x) + lane_off + 32 * q, v);
           }
         }
         tmem_wait_st();
         tc_fence_before_sync();
         mbar_arrive(bar(kBarPFull + x));
       }
+      if (i0 < i1)
+        mbar_wait_abortable(bar(kBarODone + x), (i1 - i0 - 1) & 1, a.timeout_ns, abort);
     } else {
       for (int j = 0; j < ntiles; ++j) {
         // S_x(j) complete also means PV_x(j-1) is: its MMA waited for that
@@ -838,7 +845,7 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         mbar_arrive(bar(kBarPFull + x));
       }
     }
-    if (ntiles > 0)
+    if (!MASK && ntiles > 0)
       mbar_wait_abortable(bar(kBarODone + x), (ntiles - 1) & 1, a.timeout_ns, abort);
   }
 
@@ -859,19 +866,15 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
       mbar_wait_bounded(bar(kBarDrain), 0, kDrainLimitNs);
     }
   }
-  // MASK: each thread's l for the row's other thread, over the (consumed) query tiles
-  float* pair_l = reinterpret_cast<float*>(smem_raw + (sbase - sraw));
-  if (MASK && warp < NSM) pair_l[(x_me * 2 + half_me) * kRows + row_me] = l_run;
   __syncthreads();                           // drains done
   tc_fence_after_sync();
   const bool dead = *abort;
   const bool empty = ntiles == 0;            // an empty split: m = -inf, l = 0, o = 0
-  bool odd = false;                          // MASK: a non-finite value in this thread's part
-  if (warp < NSM) {
+  if (warp < 8) {
     // ---- epilogue: out row = O / l (cascade: the partial o / l, m, l)
     const int x = x_me;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    if constexpr (MASK) l_run += pair_l[(x * 2 + 1 - half_me) * kRows + row_me];
+    bool odd = false;                        // MASK: a non-finite value in this row
     const float inv = (!dead && l_run > 0.f) ? 1.f / l_run : 0.f;
     const int h = kvh * G + row_me % G;
     const size_t orow_idx = static_cast<size_t>(q0 + tok_me) * a.num_heads + h;
@@ -881,8 +884,7 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
       a.part_l[split_rows + orow_idx] = (dead || empty) ? 0.f : l_run;
     }
 #pragma unroll
-    for (int ih = 0; ih < 4 / HALVES; ++ih) {
-      const int i = MASK ? half_me * (4 / HALVES) + ih : ih;
+    for (int i = 0; i < 4; ++i) {
       float v[32];
       tmem_ld32(t_o(x) + lane_off + 32 * i, v);
       tmem_wait_ld();
@@ -916,26 +918,20 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         }
       }
     }
-    if constexpr (MASK)
-      pair_l[512 + (x_me * 2 + half_me) * kRows + row_me] = odd && !dead && row_valid ? 1.f : 0.f;
-  }
-  tc_fence_before_sync();
-  __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-  if constexpr (MASK) {                      // the rows that came out non-finite, once more
-    if (warp < NSM && half_me == 0) {
-      const float* flag = pair_l + 512 + x_me * 2 * kRows + row_me;
-      uint32_t again = __ballot_sync(FULL, flag[0] != 0.f || flag[kRows] != 0.f);
+    if constexpr (MASK) {                    // the rows that came out non-finite, once more
+      uint32_t again = __ballot_sync(FULL, odd && !dead && row_valid);
       while (again) {
         const int src = __ffs(again) - 1;
         again &= again - 1;
-        masked_row<QT>(a, table, __shfl_sync(FULL, q0 + tok_me, src),
-                       __shfl_sync(FULL, kvh * G + row_me % G, src), kvh,
+        masked_row<QT>(a, table, __shfl_sync(FULL, q0 + tok_me, src), __shfl_sync(FULL, h, src), kvh,
                        __shfl_sync(FULL, row_pos, src), __shfl_sync(FULL, row_lo, src),
                        __shfl_sync(FULL, row_hi, src));
       }
     }
   }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 cudaError_t make_q_map(CUtensorMap* map, const void* q, int total_q, int num_heads, int G) {
