@@ -385,17 +385,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return row;
     };
+    // lane b loads box b (one lane for all of them took ~100 clocks a box, which kept V
+    // from arriving in time)
     auto load_tile = [&](const CUtensorMap* map, uint32_t dst, int row, uint32_t full) {
-#pragma unroll 1
-      for (int b = 0; b < NBOX; ++b) {
-        const int rb = __shfl_sync(FULL, row, b);
-        if (lane == 0) {
-          if (b == 0) mbar_arrive_expect_tx(full, kKvTile);
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d(dst + static_cast<uint32_t>(h * kKvHalf + b * BOXH * 128), map, h * 64,
-                        kvh, rb, full, pol);
-        }
+      if (lane == 0) mbar_arrive_expect_tx(full, kKvTile);
+      __syncwarp();
+      if (lane < NBOX) {
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(dst + static_cast<uint32_t>(h * kKvHalf + lane * BOXH * 128), map, h * 64,
+                      kvh, row, full, pol);
       }
+      __syncwarp();
     };
     // K(j), then V(j - 1): the S product of a tile comes one step before its PV
     int row_prev = 0;
