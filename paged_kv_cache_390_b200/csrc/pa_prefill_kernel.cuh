@@ -91,6 +91,9 @@ constexpr int kSmemBytes = kVOff + kVst * kKvTile + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;        // S_A, S_B, O_A, O_B: 128 columns each
 constexpr int kThreads = 320;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kPvWarp = 10;                // MOD >= 0: a warp of its own issues P V
+template <int MOD>
+__host__ __device__ constexpr int prefill_threads() { return MOD >= 0 ? kThreads + 32 : kThreads; }
 // MOD >= 0: the KV tiles' two 64-token halves are steps of their own, with S and P apart
 // in TMEM (S_A, S_B, P_A, P_B: 64 columns each, O_A, O_B: 128), so that the next step's S
 // can be computed while this one's softmax runs.
@@ -154,7 +157,7 @@ enum {
   kBarVEmpty = kBarVFull + kVst, kBarSFull = kBarVEmpty + kVst, kBarPFull = kBarSFull + 2,
   kBarODone = kBarPFull + 2, kBarDrain = kBarODone + 2,
   kBarSFree = kBarDrain + 1,                 // MOD >= 0: S is in the softmax's registers
-  kNumBars = kBarSFree + 2
+  kBarDrainPv = kBarSFree + 2, kNumBars
 };
 
 // MOD >= 0: y -> factor * tanh(y) for |y| <= 1, as factor * y * Q(y^2): Q of degree 5
@@ -230,7 +233,7 @@ __device__ __noinline__ void masked_row(const PrefillArgs& a, const int32_t* tab
 
 // BSC: tokens per block, 0: a.block_size.
 template <typename QT, int BSC, int MOD = -1>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PrefillArgs a) {
   constexpr bool MASK = MOD >= 0, CAP = MASK && (MOD & 1), BIAS = MASK && (MOD & 2);
@@ -312,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool from_threads = (i >= kBarPFull && i < kBarPFull + 2) || i >= kBarSFree;
+      const bool from_threads = (i >= kBarPFull && i < kBarPFull + 2) ||
+                                (i >= kBarSFree && i < kBarSFree + 2);
       mbar_init(bar(i), from_threads ? kRows : 1);
     }
     abort_flag = 0;
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       row_prev = row;
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t idesc_s = umma_idesc_f16(kBf16, false, kRows, kBN);
     const uint32_t idesc_o = umma_idesc_f16(kBf16, true, kRows, kD);
@@ -495,43 +499,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit_warp(bar(kBarODone + x));
       };
-      bool ok = wait1(kBarQ, 0);
-      if (ok && i0 < i1) ok = wait1(kBarKFull, 0);
-      if (ok && i0 < i1) {
-        sub_s(0, i0);
-        sub_s(1, i0);
-        if ((i0 & 1) || i0 + 1 == i1) umma_commit_warp(bar(kBarKEmpty));
-      }
-      for (int i = i0; ok && i < i1; ++i) {
-        const int j = i >> 1, vs = j % kVst, n = i - i0;
-        if (i + 1 < i1) {                    // the next step's S, once this one's is read
-          const int jn = (i + 1) >> 1;
-          if (jn != j && !(ok = wait1(kBarKFull + jn % kKst, (jn / kKst) & 1))) break;
-          if (!(ok = wait1(kBarSFree + 0, n & 1))) break;
-          sub_s(0, i + 1);
-          if (!(ok = wait1(kBarSFree + 1, n & 1))) break;
-          sub_s(1, i + 1);
-          if (((i + 1) & 1) || i + 2 == i1) umma_commit_warp(bar(kBarKEmpty + jn % kKst));
+      // S and P V each from a warp of its own: one warp for both spent as long on its
+      // waits as the tensor core on the products
+      if (warp == kMmaWarp) {
+        bool ok = wait1(kBarQ, 0);
+        for (int i = i0; ok && i < i1; ++i) {
+          const int j = i >> 1, n = i - i0;
+          if ((i == i0 || !(i & 1)) && !(ok = wait1(kBarKFull + j % kKst, (j / kKst) & 1))) break;
+          if (n > 0 && !(ok = wait1(kBarSFree + 0, (n - 1) & 1))) break;
+          sub_s(0, i);
+          if (n > 0 && !(ok = wait1(kBarSFree + 1, (n - 1) & 1))) break;
+          sub_s(1, i);
+          if ((i & 1) || i + 1 == i1) umma_commit_warp(bar(kBarKEmpty + j % kKst));
         }
-        if (i == i0 || !(i & 1)) {           // the tile's V, at its first step
-          if (!(ok = wait1(kBarVFull + vs, (j / kVst) & 1))) break;
-          const int first = max(0, u_lo - (t_lo + j) * kBN), last = min(kBN, u_hi - (t_lo + j) * kBN);
-          if (first > 0 || last < kBN) {     // rows that no row of the CTA sees: zeros
-            for (int idx = lane; idx < kBN * 16; idx += 32) {
-              const int row = idx / 16, ch = idx % 16;
-              if (row >= first && row < last) continue;
-              const uint32_t addr = v_s(vs) + (ch >> 3) * kKvHalf + row * 128 + (ch & 7) * 16;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+      } else {
+        bool ok = true;
+        for (int i = i0; ok && i < i1; ++i) {
+          const int j = i >> 1, vs = j % kVst, n = i - i0;
+          if (i == i0 || !(i & 1)) {         // the tile's V, at its first step
+            if (!(ok = wait1(kBarVFull + vs, (j / kVst) & 1))) break;
+            const int first = max(0, u_lo - (t_lo + j) * kBN), last = min(kBN, u_hi - (t_lo + j) * kBN);
+            if (first > 0 || last < kBN) {   // rows that no row of the CTA sees: zeros
+              for (int idx = lane; idx < kBN * 16; idx += 32) {
+                const int row = idx / 16, ch = idx % 16;
+                if (row >= first && row < last) continue;
+                const uint32_t addr = v_s(vs) + (ch >> 3) * kKvHalf + row * 128 + (ch & 7) * 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
             }
-            fence_proxy_async_smem();
-            __syncwarp();
           }
+          if (!(ok = wait1(kBarPFull + 0, n & 1))) break;
+          sub_pv(0, i);
+          if (!(ok = wait1(kBarPFull + 1, n & 1))) break;
+          sub_pv(1, i);
+          if ((i & 1) || i + 1 == i1) umma_commit_warp(bar(kBarVEmpty + vs));
         }
-        if (!(ok = wait1(kBarPFull + 0, n & 1))) break;
-        sub_pv(0, i);
-        if (!(ok = wait1(kBarPFull + 1, n & 1))) break;
-        sub_pv(1, i);
-        if ((i & 1) || i + 1 == i1) umma_commit_warp(bar(kBarVEmpty + vs));
       }
     }
     bool ok = !MASK && wait1(kBarQ, 0);
@@ -851,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();                           // every role is done issuing and waiting
-  if (*abort && (lane == 0 || warp == kMmaWarp)) {
+  if (*abort && (lane == 0 || warp == kMmaWarp || warp == kPvWarp)) {
     if (warp == kTmaWarp) {                  // let the copies in flight land
       for (int st = 0; st < kKst; ++st)
         if (armed_k[st] >= 0)
@@ -864,6 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       umma_commit_warp(bar(kBarDrain));
       mbar_wait_bounded(bar(kBarDrain), 0, kDrainLimitNs);
+    } else if (warp == kPvWarp) {
+      umma_commit_warp(bar(kBarDrainPv));
+      mbar_wait_bounded(bar(kBarDrainPv), 0, kDrainLimitNs);
     }
   }
   __syncthreads();                           // drains done

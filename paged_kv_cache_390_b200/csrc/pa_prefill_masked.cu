@@ -30,7 +30,7 @@ cudaError_t launch_mod(const PrefillArgs& a, int max_query_len, cudaStream_t str
   if (e != cudaSuccess) return e;
   const int rows_per_cta = kQTiles * (kRows / G);
   const dim3 grid((max_query_len + rows_per_cta - 1) / rows_per_cta, a.num_kv_heads, a.num_seqs);
-  return launch_kernel(kern, grid, dim3(kThreads), kSmemBytes, stream, pdl_mode() != 0, mq, mk, mv,
+  return launch_kernel(kern, grid, dim3(prefill_threads<MOD>()), kSmemBytes, stream, pdl_mode() != 0, mq, mk, mv,
                        a);
 }
 
