@@ -46,6 +46,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DecodeArgs a) {
   using T = Tr<KIND, D, BS>;
+  using CT = mma_type<QT, KIND, MASK>;        // MMA operand type
+  constexpr bool WIDE = !std::is_same<CT, QT>::value;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kMaxWarps * kMaxStages];
   __shared__ int stage_ok[kMaxWarps * kMaxStages];
@@ -220,13 +222,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     if (i_last < npro) issue(i_last, i_last);
   }
 
-  WarpAttn<QT, KIND, D, BS> wa;
+  WarpAttn<CT, KIND, D, BS> wa;
   wa.reset();
-  wa.load_q_global(reinterpret_cast<const QT*>(a.q) +
-                       (static_cast<size_t>(seq) * a.num_heads + static_cast<size_t>(kvh) * G + r) * D,
-                   r < G, c);
-
+  const QT* qrow = reinterpret_cast<const QT*>(a.q) +
+                   (static_cast<size_t>(seq) * a.num_heads + static_cast<size_t>(kvh) * G + r) * D;
   ScoreMod mod;
+  if constexpr (WIDE) wa.load_q_wide(qrow, r < G, c, mod.qs);
+  else wa.load_q_global(qrow, r < G, c);
+
   if constexpr (MASK) {
     mod.cap_in = a.cap_in;
     mod.cap_log2 = a.cap_log2;
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     const int nv = min(16, ntok - j * 16);
     const int okm = ok_slot[si];
     TileFrag<KIND, D, BS> fr;
-    load_tile<QT, KIND, D, BS>(fr, st, lane);
+    load_tile<CT, KIND, D, BS>(fr, st, lane);
     __syncwarp();
     if (i + S < nmine) issue(i + S, si);          // refill the stage right away
     if constexpr (MASK) {
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
       mod.lo = lo - t0;
       mod.room = a.score_stride - t0;
       if (a.scores_out) mod.logits = a.logits + (unit * a.score_stride + t0) * G;
-      tile_compute<QT, KIND, D, BS, true>(wa, fr, nv, okm, a.scale_log2, lane, mod);
+      tile_compute<CT, KIND, D, BS, true, WIDE>(wa, fr, nv, okm, a.scale_log2, lane, mod);
     } else {
       tile_compute<QT, KIND, D, BS>(wa, fr, nv, okm, a.scale_log2, lane);
     }
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     if (lane == 0) report_error(a.err_flag, kErrTimeout);
     wa.reset();
   } else {
-    wa.finish();
+    wa.template finish<WIDE>();
   }
 
   // ---- merge the warps of the CTA through shared memory

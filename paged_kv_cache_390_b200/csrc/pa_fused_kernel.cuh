@@ -54,6 +54,8 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
     decode_fused_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ FusedArgs a) {
   using T = Tr<KIND, D, BS>;
+  using CT = mma_type<QT, KIND, MASK>;        // MMA operand type
+  constexpr bool WIDE = !std::is_same<CT, QT>::value;
   constexpr int NW = kFusedWarps;
   constexpr int STG = T::STAGE;               // K and V of one tile (+ scales)
   constexpr int REC = 8 * D + 32;             // floats per partial record
@@ -285,13 +287,13 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
     }
   };
 
-  WarpAttn<QT, KIND, D, BS> wa;
+  WarpAttn<CT, KIND, D, BS> wa;
   wa.reset();
 
   // Close the current segment (tiles j0..j1 of unit (seq, kvh)).
   auto finalize = [&](int seq, int kvh, int j0, int j1, bool first) {
     const int nt = (C[seq + 1] - C[seq]) / Hkv;
-    wa.finish();
+    wa.template finish<WIDE>();
     float l0 = wa.lsum[0], l1 = wa.lsum[1];
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
@@ -537,10 +539,10 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
         wa.reset();
       }
       // its q rows (in L2 since the tile was issued)
-      wa.load_q_global(reinterpret_cast<const QT*>(a.q) +
-                           (static_cast<size_t>(seq) * a.num_heads +
-                            static_cast<size_t>(kvh) * G + r) * D,
-                       r < G, c);
+      const QT* qrow = reinterpret_cast<const QT*>(a.q) +
+                       (static_cast<size_t>(seq) * a.num_heads + static_cast<size_t>(kvh) * G + r) * D;
+      if constexpr (WIDE) wa.load_q_wide(qrow, r < G, c, mod.qs);
+      else wa.load_q_global(qrow, r < G, c);
       cur_seq = seq;
       cur_kvh = kvh;
       seg_j0 = j;
@@ -561,10 +563,10 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
       }
     }
     TileFrag<KIND, D, BS> fr;
-    load_tile<QT, KIND, D, BS>(fr, st, lane);
+    load_tile<CT, KIND, D, BS>(fr, st, lane);
     __syncwarp();
     if (i + S < nmine) issue(i + S, si);
-    if constexpr (MASK) tile_compute<QT, KIND, D, BS, true>(wa, fr, nv, okm, a.scale_log2, lane, mod);
+    if constexpr (MASK) tile_compute<CT, KIND, D, BS, true, WIDE>(wa, fr, nv, okm, a.scale_log2, lane, mod);
     else tile_compute<QT, KIND, D, BS>(wa, fr, nv, okm, a.scale_log2, lane);
     prev_j = j;
     if (++si == S) {

@@ -107,6 +107,20 @@ __device__ __forceinline__ int qk_dim(int ks, int c) {
 template <typename QT, int KIND>
 constexpr bool kFoldV = KIND != kKind16 && std::is_same<QT, __half>::value;
 
+// The MMA type of the MASK builds: bf16 q over an 8-bit cache goes through the fp16 path
+// too (the codes widen to fp16 in one step, to bf16 in four).  What bf16 has more of is
+// range, so each query head's row is scaled by a power of two to fit (WarpAttn::
+// load_q_wide), and P * s_v by another that follows the largest V scale (vfold).
+template <typename QT, int KIND, bool MASK>
+using mma_type = typename std::conditional<MASK && KIND != kKind16, __half, QT>::type;
+
+// 2^(n - e) for x = m 2^e, 1 <= m < 2 (x > 0; the exponent clamped so that the power and
+// its inverse are normal numbers).
+__device__ __forceinline__ float pow2_to(float x, int n) {
+  const int e = max(-100, min(120, static_cast<int>(__float_as_uint(x) >> 23) - 127));
+  return __int_as_float((127 + n - e) << 23);
+}
+
 // Per-lane state of one (sequence, kv head) being accumulated by a warp.
 template <typename QT, int KIND, int D, int BS>
 struct WarpAttn {
@@ -116,8 +130,10 @@ struct WarpAttn {
   float lsum[2];                    // this lane's share of the running sum
   float lv[2];                      // INT8 under fp16 q: this lane's share of sum P'
   float oacc[T::NMT][4];            // O^T accumulator (d rows, g columns)
+  float vfold;                      // WIDE: the power of two on P * s_v (0: none yet)
 
   __device__ __forceinline__ void reset() {
+    vfold = 0.f;
     m2[0] = m2[1] = -INFINITY;
     lsum[0] = lsum[1] = 0.f;
     lv[0] = lv[1] = 0.f;
@@ -136,6 +152,36 @@ struct WarpAttn {
     }
   }
 
+  // As load_q_global from a bf16 row, each head's row scaled by a power of two so that
+  // its largest element is in [2^10, 2^11); qs receives the inverse for heads 2c, 2c + 1.
+  __device__ __forceinline__ void load_q_wide(const __nv_bfloat16* qrow, bool valid, int c,
+                                              float (&qs)[2]) {
+    float top = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < T::NKS; ++ks) {
+      uint2 w = make_uint2(0u, 0u);
+      if (valid) w = *reinterpret_cast<const uint2*>(qrow + qk_dim<T>(ks, c));
+      qf[ks][0] = w.x;
+      qf[ks][1] = w.y;
+      const float2 a = unpack2<__nv_bfloat16>(w.x), b = unpack2<__nv_bfloat16>(w.y);
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float sc = top > 0.f ? pow2_to(top, 10) : 1.f;
+#pragma unroll
+    for (int ks = 0; ks < T::NKS; ++ks) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 a = unpack2<__nv_bfloat16>(qf[ks][i]);
+        qf[ks][i] = pack2<__half>(a.x * sc, a.y * sc);
+      }
+    }
+    const float back = 1.f / sc;             // exact
+    qs[0] = __shfl_sync(0xffffffffu, back, 8 * c);
+    qs[1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+  }
+
   // q rows of the group from a shared-memory copy [G][D] of QT at `base`.
   __device__ __forceinline__ void load_q_smem(uint32_t base, int g, bool valid, int c) {
 #pragma unroll
@@ -150,12 +196,13 @@ struct WarpAttn {
   // End of a unit's tiles (before its lanes' results are combined): fp16 q over an
   // 8-bit cache accumulated sum P' (bias + code) with P' = P * s_v * VFOLD; take
   // the bias term out (INT8 codes enter as 1152 + c) and the fold factor.
+  template <bool WIDE = false>
   __device__ __forceinline__ void finish() {
     if constexpr (kFoldV<QT, KIND>) {
       constexpr uint32_t FULL = 0xffffffffu;
-      constexpr float inv = 1.f / T::VFOLD;
+      const float inv = WIDE ? (vfold > 0.f ? 1.f / vfold : 0.f) : 1.f / T::VFOLD;
       float b0 = 0.f, b1 = 0.f;
-      if constexpr (KIND == kKindI8) {
+      if constexpr (KIND == kKindI8 && !WIDE) {
         float l0 = lv[0], l1 = lv[1];
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
@@ -230,13 +277,14 @@ struct ScoreMod {
   int back;                         // the query's position - t0
   int lo;                           // first seen row (may be negative)
   int G;                            // query heads per kv head
+  float qs[2];                      // WIDE: what the q rows of heads 2c, 2c + 1 were divided by
   int room;                         // rows whose scores are kept
   float* logits;                    // null, or the scores of row 0: [row][G], log2 units
 };
 
 // Accumulate one tile into `w`.  nv = valid tokens of the tile (from its
 // start), okm = bit b set if box b was loaded (tokens of other boxes masked).
-template <typename QT, int KIND, int D, int BS, bool MASK = false>
+template <typename QT, int KIND, int D, int BS, bool MASK = false, bool WIDE = false>
 __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
                                              const TileFrag<KIND, D, BS>& f, int nv, int okm,
                                              float scale_log2, int lane,
@@ -296,6 +344,12 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
     x1 = acc0[1] + acc1[1];
     x2 = acc0[2] + acc1[2];
     x3 = acc0[3] + acc1[3];
+    if constexpr (WIDE) {
+      x0 *= mod.qs[0];
+      x1 *= mod.qs[1];
+      x2 *= mod.qs[0];
+      x3 *= mod.qs[1];
+    }
     if (mod.cap_in != 0.f) {
       const float s0 = mod.cap_in * f.ks0, s1 = mod.cap_in * f.ks1;
       x0 = mod.cap_log2 * tanh_f32(x0 * s0);
@@ -350,7 +404,7 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   float p2 = fast_exp2(x2 - ms0), p3 = fast_exp2(x3 - ms1);
   w.lsum[0] = w.lsum[0] * al0 + (p0 + p2);
   w.lsum[1] = w.lsum[1] * al1 + (p1 + p3);
-  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8) {
+  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8 && !WIDE) {
     w.lv[0] *= al0;
     w.lv[1] *= al1;
   }
@@ -368,8 +422,26 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   if constexpr (T::QUANT) {
     // the V scale of each token rides on its P (fp32; poisoned scales of masked
     // tokens never reach a zero P); fp16 q also multiplies by VFOLD
-    const float v0 = kFoldV<QT, KIND> ? f.sv0 * T::VFOLD : f.sv0;
-    const float v1 = kFoldV<QT, KIND> ? f.sv1 * T::VFOLD : f.sv1;
+    float fold = T::VFOLD;
+    if constexpr (WIDE) {
+      // the power of two that brings the first V scales to [4, 8), lowered (and O with it)
+      // when a scale would come past 2^10
+      float sm = fmaxf(ok0 ? f.sv0 : 0.f, ok1 ? f.sv1 : 0.f);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) sm = fmaxf(sm, __shfl_xor_sync(FULL, sm, off));
+      if (sm > 0.f && (w.vfold == 0.f || sm * w.vfold > 1024.f)) {
+        const float to = pow2_to(sm, 2), down = w.vfold == 0.f ? 1.f : to / w.vfold;
+        w.vfold = to;
+#pragma unroll
+        for (int mt = 0; mt < T::NMT; ++mt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w.oacc[mt][k] *= down;
+        }
+      }
+      fold = w.vfold;
+    }
+    const float v0 = kFoldV<QT, KIND> ? f.sv0 * fold : f.sv0;
+    const float v1 = kFoldV<QT, KIND> ? f.sv1 * fold : f.sv1;
     p0 = p0 != 0.f ? p0 * v0 : 0.f;
     p1 = p1 != 0.f ? p1 * v0 : 0.f;
     p2 = p2 != 0.f ? p2 * v1 : 0.f;
@@ -387,7 +459,7 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   const uint32_t l23 = pack2<QT>(p2 - f23.x, p3 - f23.y);
   const uint32_t bh0 = movmatrix_trans(h01), bh1 = movmatrix_trans(h23);
   const uint32_t bl0 = movmatrix_trans(l01), bl1 = movmatrix_trans(l23);
-  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8) {
+  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8 && !WIDE) {
     // the sum of the P' the MMAs see (fp16-rounded), for the bias of the codes
     w.lv[0] += f01.x + f23.x;
     w.lv[1] += f01.y + f23.y;
@@ -426,7 +498,16 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
       for (int hh = 0; hh < 2; ++hh) {
         const int mt = 2 * q + hh;
         uint32_t af[4];
-        if constexpr (KIND == kKindI8 && std::is_same<QT, __half>::value) {
+        if constexpr (WIDE && KIND == kKindI8) {
+          // the same pairs as exact codes: the bias's own rounding (2e-5 of a V scale)
+          // would show in a bf16 output near 0
+          const uint32_t x0 = f.vf[q][2 * hh] ^ 0x80808080u;
+          const uint32_t x1 = f.vf[q][2 * hh + 1] ^ 0x80808080u;
+          af[0] = int8x2_biased_to_f16x2<0x5240u>(x0);
+          af[1] = int8x2_biased_to_f16x2<0x5341u>(x0);
+          af[2] = int8x2_biased_to_f16x2<0x5240u>(x1);
+          af[3] = int8x2_biased_to_f16x2<0x5341u>(x1);
+        } else if constexpr (KIND == kKindI8 && std::is_same<QT, __half>::value) {
           // pairs {0,2} and {1,3} of each word as fp16 1152 + c (one permute each;
           // the bias comes out once per unit, in finish())
           const uint32_t x0 = f.vf[q][2 * hh] ^ 0x80808080u;
