@@ -28,7 +28,10 @@
 // MASK (pa_decode_masked): the scores go through a tanh cap and a bias by distance, each
 // sequence's tiles start at the 16-token boundary at or before its first seen token
 // (tokens before it are masked like those past the end), and with running scores asked
-// for, the scores x and each row's log-sum-exp go to the workspace.
+// for, the scores x go to the workspace.  A split unit's records are merged by the next
+// launch (masked_finish_kernel), which finds them from the tile prefix that CTA 0 leaves
+// in place of the counters: one warp merging a unit here took 0.5 us a record, 65 us for
+// 2 sequences of 1000 tokens.
 #pragma once
 
 #include <atomic>
@@ -138,11 +141,16 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
     }
     if (threadIdx.x == blockDim.x - 1) C[NS] = wpre + incl;
     __syncthreads();
+    if constexpr (MASK) {
+      if (blockIdx.x == 0)
+        for (int s = threadIdx.x; s <= NS; s += blockDim.x) a.counters[s] = C[s];
+    }
   }
 
   // ---- this warp's equal share of the tile list
   const long long Ttot = C[NS];
-  const long long W = static_cast<long long>(gridDim.x) * NW;
+  const long long W = MASK ? masked_warps_used(Ttot, static_cast<long long>(gridDim.x) * NW)
+                           : static_cast<long long>(gridDim.x) * NW;
   const long long wme = static_cast<long long>(blockIdx.x) * NW + warp;
   // warp w gets tiles [w*q + min(w, rem), ...) with q = T / W, rem = T % W: the
   // first rem warps take one extra tile, and no empty range sits between two
@@ -152,8 +160,9 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
   auto warp_of = [&](long long g) {
     return g < (q_per + 1) * rem ? g / (q_per + 1) : rem + (g - (q_per + 1) * rem) / q_per;
   };
-  const int t_lo = static_cast<int>(range_start(wme));
-  const int nmine = static_cast<int>(range_start(wme + 1) - t_lo);
+  const bool idle = MASK && wme >= W;             // a short batch leaves warps without a share
+  const int t_lo = idle ? 0 : static_cast<int>(range_start(wme));
+  const int nmine = idle ? 0 : static_cast<int>(range_start(wme + 1) - t_lo);
 
   // Window: lane l describes tile (32 * window + l) of this warp's range.
   struct Win {
@@ -356,6 +365,7 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
       rec[8 * D + 8 + 2 * c] = l0;
       rec[8 * D + 8 + 2 * c + 1] = l1;
     }
+    if constexpr (MASK) return;
     __threadfence();
     __syncwarp();
     int prev = 0;
@@ -476,19 +486,15 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
         }
       }
     }
-    if ((a.part_o || (MASK && a.lse)) && lane < G) {
+    if (a.part_o && lane < G) {
       float M = Mg[0], L = Lg[0];
 #pragma unroll
       for (int gg = 1; gg < 8; ++gg) {
         M = lane == gg ? Mg[gg] : M;
         L = lane == gg ? Lg[gg] : L;
       }
-      if constexpr (MASK) {
-        a.lse[prow + lane] = L > 0.f ? M + log2f(L) : -INFINITY;
-      } else {
-        a.part_m[prow + lane] = M;
-        a.part_l[prow + lane] = L;
-      }
+      a.part_m[prow + lane] = M;
+      a.part_l[prow + lane] = L;
     }
     __syncwarp();
     // the records are dead: drop their L2 lines so they are never written back
@@ -593,8 +599,10 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
   }
 }
 
+// grid (may be null): the CTAs launched.
 template <typename QT, int KIND, int D, int BS, bool MASK>
-cudaError_t launch_fused_t(const FusedArgs& a0, size_t ws_bytes, cudaStream_t stream) {
+cudaError_t launch_fused_t(const FusedArgs& a0, size_t ws_bytes, cudaStream_t stream,
+                           int* grid = nullptr) {
   using T = Tr<KIND, D, BS>;
   FusedArgs a = a0;
   CUtensorMap mk, mv;
@@ -603,7 +611,7 @@ cudaError_t launch_fused_t(const FusedArgs& a0, size_t ws_bytes, cudaStream_t st
   e = make_cache_map<KIND, D, BS>(&mv, a.v_cache, a.num_kv_heads, a.num_blocks);
   if (e != cudaSuccess) return e;
   const int smem = 1024 + kFusedWarps * a.stages * T::STAGE + 4 * (a.num_seqs + 1);
-  auto kern = decode_fused_kernel<QT, KIND, D, BS, 1, MASK>;
+  auto kern = decode_fused_kernel<QT, KIND, D, BS, (MASK && KIND != kKind16) ? 3 : 1, MASK>;
   static int configured[64] = {0};
   static int configured3[64] = {0};
   int(*cfg)[64] = &configured;
@@ -634,11 +642,12 @@ cudaError_t launch_fused_t(const FusedArgs& a0, size_t ws_bytes, cudaStream_t st
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   if (per_sm > kFusedMaxCtasPerSm) per_sm = kFusedMaxCtasPerSm;
   if (a.ctas_per_sm > 0 && per_sm > a.ctas_per_sm) per_sm = a.ctas_per_sm;
-  if (ws_bytes < fused_workspace_bytes(a.num_seqs, a.num_kv_heads, D, sms))
-    return cudaErrorInvalidValue;
+  const int counted = MASK ? a.num_seqs + 1 : a.num_seqs;   // MASK: the tile prefix
+  if (ws_bytes < fused_workspace_bytes(counted, a.num_kv_heads, D, sms)) return cudaErrorInvalidValue;
   char* ws = reinterpret_cast<char*>(a.counters);
-  a.partials = reinterpret_cast<float*>(ws + fused_counter_bytes(a.num_seqs, a.num_kv_heads));
+  a.partials = reinterpret_cast<float*>(ws + fused_counter_bytes(counted, a.num_kv_heads));
   const int use = a.sm_limit > 0 && a.sm_limit < sms ? a.sm_limit : sms;
+  if (grid) *grid = use * per_sm;
   return launch_kernel(kern, dim3(use * per_sm), dim3(kFusedWarps * 32), smem, stream, a.pdl != 0,
                        mk, mv, a);
 }

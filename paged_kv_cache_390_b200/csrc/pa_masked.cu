@@ -132,8 +132,111 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// scores_out[s, kvh, t] = scores_in + the weights of t under the kv head's query heads: one
-// thread per (token, kv head, sequence), for the forms that split a sequence over CTAs.
+// After the persistent form, per (sequence, kv head): CTA x = 0 merges the unit's records
+// by log-sum-exp into out (a unit that one warp had to itself is already there), the
+// others add the weights to the running scores, kTokens cached tokens each, from
+// log-sum-exps that every CTA takes from the records' (m, l) for itself.
+// One warp per query head of the kv head; a merge keeps 8 records' loads in flight.
+constexpr int kFinish = 256, kTokens = 1024;
+
+template <typename QT, int D>
+__global__ void __launch_bounds__(kFinish)
+    masked_finish_kernel(const __grid_constant__ MaskedArgs a, const int* __restrict__ prefix,
+                         const float* __restrict__ records, int warps) {
+  constexpr uint32_t FULL = 0xffffffffu;
+  constexpr int REC = 8 * D + 32;
+  __shared__ float lse[kMaxGroup];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int kvh = blockIdx.y, s = blockIdx.z;
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int G = a.num_heads / a.num_kv_heads;
+  const size_t row = static_cast<size_t>(s) * a.num_heads + kvh * G + g;
+  const long long total = prefix[a.num_seqs], W = masked_warps_used(total, warps);
+  const int c0 = prefix[s], nt = (prefix[s + 1] - c0) / a.num_kv_heads;
+  const long long q = total / W, rem = total % W;
+  auto range_start = [&](long long w) { return w * q + (w < rem ? w : rem); };
+  auto warp_of = [&](long long t) {
+    return t < (q + 1) * rem ? t / (q + 1) : rem + (t - (q + 1) * rem) / q;
+  };
+  const long long start = c0 + static_cast<long long>(kvh) * nt;
+  const long long wf = nt > 0 ? warp_of(start) : 0, wl = nt > 0 ? warp_of(start + nt - 1) : 0;
+  const int n = nt > 0 ? static_cast<int>(wl - wf + 1) : 0;      // records (1: none was left)
+  const int slot_f = nt > 0 && range_start(wf) == start ? 0 : 1;
+  auto record = [&](int t) {
+    return records + static_cast<size_t>(2 * (wf + t) + (t == 0 ? slot_f : 0)) * REC;
+  };
+  float M = -INFINITY, L = 0.f;
+  if (n > 1 && g < G) {
+    for (int t = lane; t < n; t += 32) M = fmaxf(M, record(t)[8 * D + g]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    if (M != -INFINITY)
+      for (int t = lane; t < n; t += 32)
+        L += record(t)[8 * D + 8 + g] * fast_exp2(record(t)[8 * D + g] - M);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+  }
+  if (blockIdx.x == 0) {
+    if (n <= 1 || g >= G) return;
+    constexpr int L4 = D / 4, PER = 32 / L4;     // lanes of a row, rows a warp takes at once
+    const int d4 = lane % L4, sub = lane / L4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int t0 = sub; t0 < n; t0 += 8 * PER) {
+      float m[8];
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int t = t0 + u * PER;
+        m[u] = t < n ? record(t)[8 * D + g] : -INFINITY;
+        v[u] = t < n ? reinterpret_cast<const float4*>(record(t) + g * D)[d4]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = M == -INFINITY ? 0.f : fast_exp2(m[u] - M);
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+    }
+    if constexpr (PER == 2) {
+      acc.x += __shfl_xor_sync(FULL, acc.x, 16);
+      acc.y += __shfl_xor_sync(FULL, acc.y, 16);
+      acc.z += __shfl_xor_sync(FULL, acc.z, 16);
+      acc.w += __shfl_xor_sync(FULL, acc.w, 16);
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays NaN
+    if (sub == 0) {
+      uint2 pk;
+      pk.x = pack2<QT>(acc.x * inv, acc.y * inv);
+      pk.y = pack2<QT>(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<QT*>(a.out) + row * D + 4 * d4) = pk;
+    }
+    return;
+  }
+  const int len = a.seq_lens[s];
+  if (len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_blocks) * a.block_size)
+    return;                                       // a skipped sequence keeps its scores
+  const int have = min(len, a.score_stride), from = (blockIdx.x - 1) * kTokens;
+  if (from >= have) return;
+  if (g < G && lane == 0)
+    lse[g] = n == 1 ? a.lse[row] : (L > 0.f ? M + log2f(L) : -INFINITY);
+  __syncthreads();
+  const int lo = seen_span(a.kv_start ? a.kv_start[s] : 0, len - 1, a.window, 0, len).lo;
+  const size_t unit = (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride;
+#pragma unroll
+  for (int u = 0; u < kTokens / kFinish; ++u) {
+    const int t = from + u * kFinish + threadIdx.x;
+    if (t >= have) break;
+    const float before = a.scores_in ? a.scores_in[unit + t] : 0.f;
+    a.scores_out[unit + t] =
+        before + (t >= lo ? token_weight(a.logits + (unit + t) * G, lse, G) : 0.f);
+  }
+}
+
+// fp32 caches' running scores: one thread per (token, kv head, sequence).
 __global__ void __launch_bounds__(256)
     masked_scores_kernel(const __grid_constant__ MaskedArgs a) {
   __shared__ float lse[kMaxGroup];
@@ -189,11 +292,11 @@ namespace {
 
 template <typename QT, int KIND>
 cudaError_t masked_shape(const FusedArgs& a, int D, int BS, size_t ws, cudaStream_t s,
-                         const DecodeArgs* v1, const DecodeShape& sh) {
+                         const DecodeArgs* v1, const DecodeShape& sh, int* grid) {
 #define PA_CASE(DD, BB) \
   if (D == DD && BS == BB)                                                             \
     return v1 ? launch_tc<QT, KIND, DD, BB, true>(*v1, sh, s)                          \
-              : launch_fused_t<QT, KIND, DD, BB, true>(a, ws, s);
+              : launch_fused_t<QT, KIND, DD, BB, true>(a, ws, s, grid);
   PA_CASE(128, 16)
   PA_CASE(128, 8)
   PA_CASE(128, 32)
@@ -207,17 +310,17 @@ cudaError_t masked_shape(const FusedArgs& a, int D, int BS, size_t ws, cudaStrea
 // The persistent form, or with v1 the one-CTA-per-(sequence, kv head) form.
 cudaError_t launch_masked_tc(const FusedArgs& a, int q_dtype, int cache_dtype, int D, int BS,
                              size_t ws, cudaStream_t s, const DecodeArgs* v1,
-                             const DecodeShape& sh) {
+                             const DecodeShape& sh, int* grid) {
   const bool qh = q_dtype == PA_F16;
   switch (cache_dtype) {
-    case PA_F16: return masked_shape<__half, kKind16>(a, D, BS, ws, s, v1, sh);
-    case PA_BF16: return masked_shape<__nv_bfloat16, kKind16>(a, D, BS, ws, s, v1, sh);
+    case PA_F16: return masked_shape<__half, kKind16>(a, D, BS, ws, s, v1, sh, grid);
+    case PA_BF16: return masked_shape<__nv_bfloat16, kKind16>(a, D, BS, ws, s, v1, sh, grid);
     case PA_INT8:
-      return qh ? masked_shape<__half, kKindI8>(a, D, BS, ws, s, v1, sh)
-                : masked_shape<__nv_bfloat16, kKindI8>(a, D, BS, ws, s, v1, sh);
+      return qh ? masked_shape<__half, kKindI8>(a, D, BS, ws, s, v1, sh, grid)
+                : masked_shape<__nv_bfloat16, kKindI8>(a, D, BS, ws, s, v1, sh, grid);
     case PA_FP8E4M3:
-      return qh ? masked_shape<__half, kKindE4M3>(a, D, BS, ws, s, v1, sh)
-                : masked_shape<__nv_bfloat16, kKindE4M3>(a, D, BS, ws, s, v1, sh);
+      return qh ? masked_shape<__half, kKindE4M3>(a, D, BS, ws, s, v1, sh, grid)
+                : masked_shape<__nv_bfloat16, kKindE4M3>(a, D, BS, ws, s, v1, sh, grid);
   }
   return cudaErrorInvalidValue;
 }
@@ -243,10 +346,11 @@ size_t lse_bytes(int num_seqs, int num_heads) {
 }
 }  // namespace
 
-// The persistent decode's workspace, then lse, then the scores x of every cached token.
+// The persistent decode's workspace (the tile prefix, then the records), then lse, then
+// the scores x of every cached token.
 size_t masked_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                               int score_width, int num_sms) {
-  return fused_workspace_bytes(num_seqs, num_kv_heads, head_dim, num_sms) +
+  return fused_workspace_bytes(num_seqs + 1, num_kv_heads, head_dim, num_sms) +
          lse_bytes(num_seqs, num_heads) +
          static_cast<size_t>(num_seqs) * num_heads * score_width * sizeof(float);
 }
@@ -256,7 +360,7 @@ cudaError_t launch_decode_masked(const MaskedArgs& a0, int q_dtype, int cache_dt
   MaskedArgs a = a0;
   if (a.scores_out) {
     char* ws = static_cast<char*>(workspace) +
-               fused_workspace_bytes(a.num_seqs, a.num_kv_heads, head_dim, num_sms);
+               fused_workspace_bytes(a.num_seqs + 1, a.num_kv_heads, head_dim, num_sms);
     a.lse = reinterpret_cast<float*>(ws);
     a.logits = reinterpret_cast<float*>(ws + lse_bytes(a.num_seqs, a.num_heads));
   }
@@ -328,10 +432,27 @@ cudaError_t launch_decode_masked(const MaskedArgs& a0, int q_dtype, int cache_dt
       d.logits = a.logits;
       d.score_stride = a.score_stride;
     }
+    int ctas = 0;
     e = launch_masked_tc(f, q_dtype, cache_dtype, head_dim, a.block_size,
-                         fused_workspace_bytes(a.num_seqs, a.num_kv_heads, head_dim, num_sms), s,
-                         one_cta ? &d : nullptr, sh);
-    if (one_cta) return e;                   // its CTAs add the running scores themselves
+                         fused_workspace_bytes(a.num_seqs + 1, a.num_kv_heads, head_dim, num_sms), s,
+                         one_cta ? &d : nullptr, sh, &ctas);
+    if (one_cta || e != cudaSuccess) return e;   // its CTAs add the running scores themselves
+    const float* records = reinterpret_cast<const float*>(
+        static_cast<char*>(workspace) + fused_counter_bytes(a.num_seqs + 1, a.num_kv_heads));
+    const int* prefix = static_cast<const int*>(workspace);
+    int chunks = 0;
+    if (a.scores_out) {
+      const long long cap = static_cast<long long>(a.max_blocks) * a.block_size;
+      chunks = static_cast<int>(((cap < a.score_stride ? cap : a.score_stride) + kTokens - 1) / kTokens);
+    }
+    const dim3 grid(1 + chunks, a.num_kv_heads, a.num_seqs);
+    const bool pdl = pdl_mode() != 0, wide = head_dim == 128;
+    auto kern = q_dtype == PA_BF16 ? (wide ? masked_finish_kernel<__nv_bfloat16, 128>
+                                           : masked_finish_kernel<__nv_bfloat16, 64>)
+                                   : (wide ? masked_finish_kernel<__half, 128>
+                                           : masked_finish_kernel<__half, 64>);
+    return launch_kernel(kern, grid, dim3(kFinish), 0, s, pdl, a, prefix, records,
+                         ctas * kFusedWarps);
   }
   if (e != cudaSuccess || !a.scores_out) return e;
   const long long cap = static_cast<long long>(a.max_blocks) * a.block_size;

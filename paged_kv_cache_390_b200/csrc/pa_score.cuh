@@ -44,6 +44,13 @@ __device__ __forceinline__ float tanh_f32(float y) {
   return a < 0.625f ? fmaf(y * z, q, y) : big;
 }
 
+// Warps that share out `tiles` 16-token tiles: all of them, but at least 4 tiles each (a
+// record to write and merge costs about as much as a tile or two).
+__host__ __device__ __forceinline__ long long masked_warps_used(long long tiles, long long warps) {
+  const long long most = (tiles + 3) / 4;
+  return most < 1 ? 1 : (most < warps ? most : warps);
+}
+
 // A cached token's weight summed over the G query heads of its kv head, from their scores
 // x and log-sum-exps (log2 units; -inf: that head's row saw nothing).
 __device__ __forceinline__ float token_weight(const float* x, const float* lse, int G) {
