@@ -330,15 +330,23 @@ int masked_warps(int cache_dtype) {
   return cache_dtype == PA_INT8 || cache_dtype == PA_FP8E4M3 ? kMaxWarps : kDefaultWarps;
 }
 
-// One CTA per (sequence, kv head) where that fills the GPU with short ones, or where
-// there is little to split; else the persistent form, which spreads long or few ones over
-// every SM.
+// One CTA per (sequence, kv head), or the persistent form, which spreads long or few units
+// over every SM at the price of a second launch.  By the most tiles a unit can have
+// (table width or window); device times, one CTA / persistent, lengths even in [L/2, L]:
+//   16-bit, 64/8 heads   L 768: 8.8 / 12.1 us (2 sequences), 17.7 / 22.4 (32), 32.1 / 34.6 (64)
+//                        L 1500: 20.5 / 14.2 (2), 24.9 / 24.3 (19), 30.0 / 32.0 (32)
+//                        L 3000: 38.3 / 20.4 (2), 45.5 / 35.7 (19), 97.2 / 97.6 (64)
+//   FP8, 32/8 heads      L 512: 9.4 / 9.4 (2), L 1500: 16.1 / 14.3 (2), 51.3 / 53.5 (64)
+// Under a window the lengths are alike and the CTAs even: 64 sequences, window 4096, FP8:
+// 144.8 / 156.4.
 bool pick_one_cta(const MaskedArgs& a, int cache_dtype, int num_sms) {
   long long most = static_cast<long long>(a.max_blocks) * a.block_size;   // tokens a row sees
-  if (a.window > 0 && a.window + 15LL < most) most = a.window + 15LL;
+  const bool even = a.window > 0 && a.window + 15LL < most;
+  if (even) most = a.window + 15LL;
   const long long tiles = (most + 15) / 16;
   const long long units = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
-  return (units >= num_sms && tiles <= 256) || tiles <= 4 * masked_warps(cache_dtype);
+  return tiles <= 8 * masked_warps(cache_dtype) ||
+         (2 * units >= 3LL * num_sms && tiles <= (even ? 288 : 192));
 }
 
 size_t lse_bytes(int num_seqs, int num_heads) {

@@ -154,11 +154,19 @@ FORMS = {
 LENS = [1, 15, 16, 17, 33, 100, 255, 300, 0, 700]
 
 
+def _wide(b, tokens=1024):
+    """A table for more tokens than any sequence has: the persistent form."""
+    b.table = torch.nn.functional.pad(b.table, (0, tokens // b.bs), value=-1)
+
+
 @pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
 @pytest.mark.parametrize("form", sorted(FORMS))
 @pytest.mark.parametrize("dt,cd", PAIRS)
-def test_decode(pa, dt, cd, form):
-    b = Batch(dt, cd, LENS, [1 if n else 1 for n in LENS], 16, 2, 128, 16, 11, **FORMS[form])
+def test_decode(pa, dt, cd, form, wide):
+    b = Batch(dt, cd, LENS, [1] * len(LENS), 16, 2, 128, 16, 11, **FORMS[form])
+    if wide:
+        _wide(b)
     b.rows[8] = (torch.zeros(1, dtype=torch.long), torch.zeros(1, dtype=torch.long), torch.tensor([-1]))
     _close(_decode(pa, b), b, form)
 
@@ -176,7 +184,7 @@ def test_decode_documents_and_scores(pa, dt, cd, D, bs, wide):
     starts = [0, 15, 17, 16, -4, 127, 250, 50, 90]
     b = Batch(dt, cd, lens, [1] * len(lens), 12, 4, D, bs, D + bs, softcap=20.0, starts=starts)
     if wide:
-        b.table = torch.nn.functional.pad(b.table, (0, 1024 // bs), value=-1)
+        _wide(b)
     width = 310
     g = torch.Generator().manual_seed(3)
     before = torch.rand((len(lens), 4, width), generator=g)
@@ -231,6 +239,43 @@ def test_decode_large_logits_under_the_cap(pa):
     """Scores far past the cap: the tanh is flat there and every score is near +-cap."""
     b = Batch("bf16", "bf16", [70, 200], [1, 1], 8, 2, 128, 16, 5, softcap=8.0, qmul=60.0)
     _close(_decode(pa, b), b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("cd", ["int8", "fp8"])
+@pytest.mark.parametrize("kv,qm", [(2.0 ** 40, 2.0 ** -60), (2.0 ** -40, 2.0 ** 30), (1.0, 2.0 ** -20)])
+def test_decode_bf16_range_over_8_bit_caches(pa, cd, kv, qm, wide):
+    """bf16's range, which fp16 lacks, on both sides: huge or tiny K and V scales and
+    queries, and a V scale that grows by 2^30 in the middle of a sequence."""
+    b = Batch("bf16", cd, [300, 40], [1, 1], 8, 2, 64, 16, 17)
+    grow = torch.ones(b.sc[1].shape)
+    blk = [int(x) for x in b.table[0] if x >= 0]
+    grow[blk[9]:blk[9] + 1] = 2.0 ** 30
+    for i in range(2):
+        b.sc[i] = b.sc[i] * kv * (grow if i else 1.0)
+        b.val[i] = b.val[i] * kv * (grow.transpose(1, 2)[..., None].double() if i else 1.0)
+    b.q = (b.q.float() * qm).to(torch.bfloat16)
+    b.scale = b.scale / (kv * qm)
+    if wide:
+        _wide(b)
+    want, tol, _ = b.want()
+    got = _decode(pa, b).cpu().double()
+    # the tolerance's floor for tiny values scales with the values
+    tol = tol + 300 * 2.0 ** -25 * want.abs().amax(-1, keepdim=True)
+    assert torch.isfinite(got).all() and ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_prefill_large_logits_and_steep_biases(pa, dt):
+    """Scores past the polynomial's range (tanh over its whole range), and a slope so
+    steep that the largest product is not the largest score."""
+    b = Batch(dt, dt, [300], [200], 8, 2, 128, 16, 5, softcap=8.0, qmul=20.0)
+    _close(_prefill(pa, b), b)
+    b = Batch(dt, dt, [300], [200], 8, 2, 128, 16, 6, alibi=True, prefix=[250], qmul=4.0)
+    b.slopes = torch.tensor([3.0, 1.0, 0.5, 0.0, -0.01, 2.0, 0.25, 1.5])
+    _close(_prefill(pa, b), b)
 
 
 @pytest.mark.gpu
