@@ -301,12 +301,12 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
  *                  pa_evict takes these scores.
  *   workspace      device memory, 256-byte aligned, at least
  *                  pa_decode_masked_workspace_bytes(num_seqs, num_heads, num_kv_heads,
- *                  head_dim, scores_out ? score_stride : 0) bytes, ZEROED BEFORE ITS FIRST
- *                  USE and after a call that reported PA_DEVERR_TIMEOUT.  Calls that share
- *                  a workspace (two captured graphs, two streams) must not overlap on the
- *                  GPU.
- *   Other arguments, types and err_flag as pa_decode_fused.  A sequence that sees nothing
- *   gets zeros.  Whatever the rows of unseen tokens hold (infinities, NaN) does not reach
+ *                  head_dim, scores_out ? score_stride : 0) bytes; needs no clearing.
+ *                  Calls that share a workspace (two captured graphs, two streams) must not
+ *                  overlap on the GPU.
+ *   Other arguments, types and err_flag as pa_decode_fused.  Short sequences take one
+ *   launch (a CTA per sequence and kv head), long or few ones two.  A sequence that sees
+ *   nothing gets zeros.  Whatever the rows of unseen tokens hold (infinities, NaN) does not reach
  *   the output or the scores.  A sequence dropped for its length (err_flag) keeps its
  *   scores.  Deterministic for a given batch.
  */
@@ -335,8 +335,9 @@ PA_API size_t pa_decode_masked_workspace_bytes(int num_seqs, int num_heads, int 
  *                  by every row of sequence s that its kv_start and window allow, later
  *                  ones too (a prefix that attends in both directions).
  *   softcap, alibi_slopes, window   as pa_decode_masked.
- *   Other arguments as pa_prefill.  Also head_dim 64, fp32, and quantised caches (k_scale,
- *   v_scale as pa_decode_v1), these on CUDA cores; num_heads / num_kv_heads <= 128.
+ *   Other arguments as pa_prefill; num_heads / num_kv_heads <= 128, any number.  Also
+ *   head_dim 64, fp32, and quantised caches (k_scale, v_scale as pa_decode_v1): these run
+ *   on the CUDA cores, one warp per row and head (about 3 TFLOP/s), for completeness.
  *   A row that sees nothing gets zeros.  Unseen rows of K and V do not reach a row's
  *   output, whatever they hold.  A sequence whose lengths or query rows are out of range
  *   is skipped, a bad block id read as zeros, as in pa_prefill.

@@ -122,50 +122,47 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _same_device(*tensors) -> torch.device:
-    """The CUDA device that all the tensors are on."""
-    first = tensors[0]
+def _same_device(dense, rows=()) -> int:
+    """Index of the CUDA device that all the tensors are on; those of `dense` contiguous."""
+    first = dense[0]
     if not first.is_cuda:
         raise ValueError("tensors passed to libpa must be CUDA tensors")
     index = first.get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
+    for t in dense:
+        if t is not None:
+            if t.get_device() != index:
+                raise ValueError("tensors of one call must be on one CUDA device")
+            if not t.is_contiguous():
+                raise ValueError("tensors passed to libpa must be contiguous")
+    for t in rows:
+        if t.get_device() != index:
             raise ValueError("tensors of one call must be on one CUDA device")
-    return first.device
+    return index
 
 
-class _on:
-    """Make `dev` current, and `stream` (if given) torch's stream there, so that what the
-    call allocates belongs to the stream that uses it; yields the stream's handle.  The
-    usual case (the current device and stream) costs one lookup of the handle."""
-    __slots__ = ("dev", "ctx")
+def _enter(index, stream):
+    """Make device `index` current, and `stream` (if given) torch's stream there, so that
+    what the call allocates belongs to the stream that uses it.  Returns the context to
+    leave again, None in the usual case (the current device and stream)."""
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError("the stream and the tensors must be on one CUDA device")
+        ctx = torch.cuda.stream(stream)
+    elif index != torch.cuda.current_device():
+        ctx = torch.cuda.device(index)
+    else:
+        return None
+    ctx.__enter__()
+    return ctx
 
-    def __init__(self, dev, stream):
-        self.dev = dev
-        self.ctx = None
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError("the stream and the tensors must be on one CUDA device")
-            self.ctx = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.dev.index)
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            return self.ctx.__exit__(*exc)
+def _leave(ctx) -> None:
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
 
 
 def _addr(t):
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to libpa must be contiguous")
-    return t.data_ptr()
+    return None if t is None else t.data_ptr()
 
 
 def _row_stride(t, T, heads, D) -> int:
@@ -267,23 +264,28 @@ def rope_and_cache(q, key, value, positions, inv_freq, pair_axis, k_cache, v_cac
             or inv_freq.dtype != torch.float64 or pair_axis.dtype != torch.int32):
         raise ValueError("positions and slots are int64, inv_freq float64, pair_axis int32")
     code = _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype)
-    dev = _same_device(q, key, value, positions, inv_freq, pair_axis, k_cache, v_cache,
-                       slot_mapping, k_scale, v_scale, err_flag, out)
-    with _on(dev, stream) as s:
+    index = _same_device((k_cache, v_cache, positions, inv_freq, pair_axis, slot_mapping, k_scale,
+                          v_scale, err_flag, out), (q, key, value))
+    strides = (_row_stride(q, num_tokens, num_heads, head_dim),
+               _row_stride(key, num_tokens, num_kv_heads, head_dim),
+               _row_stride(value, num_tokens, num_kv_heads, head_dim))
+    if out is not None and (out.shape != q.shape or out.dtype != dtype):
+        raise ValueError("out must have q's shape and dtype")
+    ctx = _enter(index, stream)
+    try:
         if out is None:
-            out = torch.empty((num_tokens, num_heads, head_dim), dtype=dtype, device=dev)
-        elif out.shape != q.shape or out.dtype != dtype:
-            raise ValueError("out must have q's shape and dtype")
-        rc = lib().pa_rope_and_cache(
-            _addr(out), q.data_ptr(), key.data_ptr(), value.data_ptr(), _FLOAT_CODES[dtype],
-            _row_stride(q, num_tokens, num_heads, head_dim),
-            _row_stride(key, num_tokens, num_kv_heads, head_dim),
-            _row_stride(value, num_tokens, num_kv_heads, head_dim), _addr(positions), num_axes,
-            _addr(inv_freq), _addr(pair_axis), 2 * pairs[0], int(bool(interleaved)),
-            _addr(k_cache), _addr(v_cache), code, _addr(k_scale), _addr(v_scale), _addr(slot_mapping),
-            num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, _addr(err_flag),
-            s)
-    _check(rc, "pa_rope_and_cache")
+            out = torch.empty((num_tokens, num_heads, head_dim), dtype=dtype, device=q.device)
+        rc = (_lib or lib()).pa_rope_and_cache(
+            out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), _FLOAT_CODES[dtype],
+            *strides, positions.data_ptr(), num_axes, inv_freq.data_ptr(), pair_axis.data_ptr(),
+            2 * pairs[0], 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), code,
+            _addr(k_scale), _addr(v_scale), slot_mapping.data_ptr(), num_tokens, num_heads,
+            num_kv_heads, head_dim, block_size, num_blocks, _addr(err_flag),
+            torch._C._cuda_getCurrentRawStream(index))
+    finally:
+        _leave(ctx)
+    if rc:
+        _check(rc, "pa_rope_and_cache")
     return out
 
 
@@ -312,8 +314,8 @@ def copy_blocks(src_k, src_v, dst_k, dst_v, block_mapping, *, cache_dtype=None,
 
 
 class MaskedWorkspace:
-    """Workspace of pa_decode_masked, zeroed once; score_width is the scores' last
-    dimension (0: calls without scores)."""
+    """Workspace of pa_decode_masked; score_width is the scores' last dimension (0: calls
+    without scores)."""
 
     def __init__(self, num_seqs, num_heads, num_kv_heads, head_dim, score_width=0, device="cuda"):
         dev = torch.device(device)
@@ -322,7 +324,8 @@ class MaskedWorkspace:
         with torch.cuda.device(dev):
             self.nbytes = int(lib().pa_decode_masked_workspace_bytes(
                 num_seqs, num_heads, num_kv_heads, head_dim, score_width))
-            self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=dev)
+            self.buf = torch.empty(max(self.nbytes, 256), dtype=torch.uint8, device=dev)
+        self.address = self.buf.data_ptr()
 
 
 def _row_ints(t, n, what):
@@ -363,22 +366,28 @@ def decode_masked(q, k_cache, v_cache, block_tables, seq_lens, scale, *, softcap
         raise ValueError("scores_in needs scores_out")
     if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
         raise ValueError("out must have q's shape and dtype")
-    dev = _same_device(q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes, kv_start,
-                       scores_in, scores_out, out, k_scale, v_scale, err_flag,
-                       workspace.buf if workspace is not None else None)
-    with _on(dev, stream) as s:
-        if workspace is None:
-            workspace = MaskedWorkspace(num_seqs, num_heads, num_kv_heads, head_dim, width, dev)
+    index = _same_device((q, k_cache, v_cache, block_tables, seq_lens, alibi_slopes, kv_start,
+                          scores_in, scores_out, out, k_scale, v_scale, err_flag,
+                          workspace.buf if workspace is not None else None))
+    ctx = _enter(index, stream)
+    try:
         if out is None:
             out = torch.empty_like(q)
-        rc = lib().pa_decode_masked(
-            _addr(out), _addr(q), _FLOAT_CODES[q.dtype], _addr(k_cache), _addr(v_cache), code,
-            _addr(k_scale), _addr(v_scale), _addr(block_tables), block_tables.shape[1],
-            _addr(seq_lens), num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks,
-            float(scale), float(softcap), _addr(alibi_slopes), _addr(kv_start), int(window),
-            _addr(scores_in), _addr(scores_out), width, _addr(workspace.buf), workspace.nbytes,
-            _addr(err_flag), s)
-    _check(rc, "pa_decode_masked")
+        if num_seqs == 0:
+            return out
+        if workspace is None:
+            workspace = MaskedWorkspace(num_seqs, num_heads, num_kv_heads, head_dim, width, q.device)
+        rc = (_lib or lib()).pa_decode_masked(
+            out.data_ptr(), q.data_ptr(), _FLOAT_CODES[q.dtype], k_cache.data_ptr(),
+            v_cache.data_ptr(), code, _addr(k_scale), _addr(v_scale), block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), num_seqs, num_heads, num_kv_heads, head_dim,
+            block_size, num_blocks, scale, softcap, _addr(alibi_slopes), _addr(kv_start), window,
+            _addr(scores_in), _addr(scores_out), width, workspace.address, workspace.nbytes,
+            _addr(err_flag), torch._C._cuda_getCurrentRawStream(index))
+    finally:
+        _leave(ctx)
+    if rc:
+        _check(rc, "pa_decode_masked")
     return out
 
 
@@ -400,21 +409,27 @@ def prefill_masked(q, k_cache, v_cache, block_tables, seq_lens, query_start, sca
     _row_ints(prefix_lens, num_seqs, "prefix_lens")
     if out is not None and (out.shape != q.shape or out.dtype != q.dtype):
         raise ValueError("out must have q's shape and dtype")
-    dev = _same_device(q, k_cache, v_cache, block_tables, seq_lens, query_start, alibi_slopes,
-                       kv_start, prefix_lens, out, k_scale, v_scale, err_flag)
-    with _on(dev, stream) as s:
-        if max_query_len is None:
-            max_query_len = (int((query_start[1:] - query_start[:-1]).max())
-                             if query_start.numel() > 1 else 0)
+    index = _same_device((q, k_cache, v_cache, block_tables, seq_lens, query_start, alibi_slopes,
+                          kv_start, prefix_lens, out, k_scale, v_scale, err_flag))
+    ctx = _enter(index, stream)
+    try:
         if out is None:
             out = torch.empty_like(q)
-        rc = lib().pa_prefill_masked(
-            _addr(out), _addr(q), _FLOAT_CODES[q.dtype], _addr(query_start), total_q,
-            int(max_query_len), _addr(k_cache), _addr(v_cache), code, _addr(k_scale), _addr(v_scale),
-            _addr(block_tables), block_tables.shape[1], _addr(seq_lens), num_seqs, num_heads,
-            num_kv_heads, head_dim, block_size, num_blocks, float(scale), float(softcap),
-            _addr(alibi_slopes), _addr(kv_start), _addr(prefix_lens), int(window), _addr(err_flag), s)
-    _check(rc, "pa_prefill_masked")
+        if num_seqs == 0 or total_q == 0:
+            return out
+        if max_query_len is None:
+            max_query_len = int((query_start[1:] - query_start[:-1]).max())
+        rc = (_lib or lib()).pa_prefill_masked(
+            out.data_ptr(), q.data_ptr(), _FLOAT_CODES[q.dtype], query_start.data_ptr(), total_q,
+            max_query_len, k_cache.data_ptr(), v_cache.data_ptr(), code, _addr(k_scale),
+            _addr(v_scale), block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+            num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, softcap,
+            _addr(alibi_slopes), _addr(kv_start), _addr(prefix_lens), window, _addr(err_flag),
+            torch._C._cuda_getCurrentRawStream(index))
+    finally:
+        _leave(ctx)
+    if rc:
+        _check(rc, "pa_prefill_masked")
     return out
 
 
@@ -430,32 +445,40 @@ def evict(k_cache, v_cache, block_tables, seq_lens, new_block_tables, scores, nu
     code = _pool_checks(k_cache, v_cache, k_scale, v_scale, cache_dtype)
     _batch_checks(block_tables, seq_lens, num_seqs)
     _batch_checks(new_block_tables, seq_lens, num_seqs)
-    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (num_seqs,
-                                                                                  num_kv_heads):
+    if (scores.dtype != torch.float32 or scores.dim() != 3
+            or scores.shape[:2] != (num_seqs, num_kv_heads)):
         raise ValueError("scores must be float32 [num_seqs, num_kv_heads, width]")
-    dev = _same_device(k_cache, v_cache, block_tables, seq_lens, new_block_tables, scores, kept,
-                       new_scores, new_lens, k_scale, v_scale, err_flag)
-    with _on(dev, stream) as s:
+    index = _same_device((k_cache, v_cache, block_tables, seq_lens, new_block_tables, scores, kept,
+                          new_scores, new_lens, k_scale, v_scale, err_flag))
+    unit = (num_seqs, num_kv_heads)
+    for t, dt in ((kept, torch.int32), (new_scores, torch.float32)):
+        if t is not None and (t.dtype != dt or t.dim() != 3 or t.shape[:2] != unit):
+            raise ValueError("kept (int32) and new_scores (float32) are "
+                             "[num_seqs, num_kv_heads, width]")
+    if new_lens is not None and (new_lens.dtype != torch.int32 or new_lens.shape != (num_seqs,)):
+        raise ValueError("new_lens must be int32 [num_seqs]")
+    ctx = _enter(index, stream)
+    try:
         if kept is None:
-            kept = torch.empty((num_seqs, num_kv_heads, num_keep), dtype=torch.int32, device=dev)
+            kept = torch.empty((*unit, num_keep), dtype=torch.int32, device=k_cache.device)
         if new_scores is None:
-            new_scores = torch.zeros((num_seqs, num_kv_heads, num_keep), device=dev)
+            new_scores = torch.zeros((*unit, num_keep), device=k_cache.device)
         if new_lens is None:
-            new_lens = torch.empty(num_seqs, dtype=torch.int32, device=dev)
-        for t, dt in ((kept, torch.int32), (new_scores, torch.float32)):
-            if t.dtype != dt or t.dim() != 3 or t.shape[:2] != scores.shape[:2]:
-                raise ValueError("kept (int32) and new_scores (float32) are "
-                                 "[num_seqs, num_kv_heads, width]")
-        if new_lens.dtype != torch.int32 or new_lens.shape != (num_seqs,):
-            raise ValueError("new_lens must be int32 [num_seqs]")
-        rc = lib().pa_evict(
-            _addr(k_cache), _addr(v_cache), code, _addr(k_scale), _addr(v_scale), _addr(block_tables),
-            block_tables.shape[1], _addr(seq_lens), _addr(new_block_tables),
-            new_block_tables.shape[1], _addr(scores), scores.shape[2], int(num_keep),
-            int(num_recent), _addr(kept), kept.shape[2], _addr(new_scores), new_scores.shape[2],
-            _addr(new_lens), num_seqs, num_kv_heads, head_dim, block_size, num_blocks,
-            _addr(err_flag), s)
-    _check(rc, "pa_evict")
+            new_lens = torch.empty(num_seqs, dtype=torch.int32, device=k_cache.device)
+        if num_seqs == 0:
+            return kept, new_lens, new_scores
+        rc = (_lib or lib()).pa_evict(
+            k_cache.data_ptr(), v_cache.data_ptr(), code, _addr(k_scale), _addr(v_scale),
+            block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+            new_block_tables.data_ptr(), new_block_tables.shape[1], scores.data_ptr(),
+            scores.shape[2], num_keep, num_recent, kept.data_ptr(), kept.shape[2],
+            new_scores.data_ptr(), new_scores.shape[2], new_lens.data_ptr(), num_seqs, num_kv_heads,
+            head_dim, block_size, num_blocks, _addr(err_flag),
+            torch._C._cuda_getCurrentRawStream(index))
+    finally:
+        _leave(ctx)
+    if rc:
+        _check(rc, "pa_evict")
     return kept, new_lens, new_scores
 
 

@@ -333,6 +333,55 @@ def test_decode_bad_blocks_and_lengths(pa, dt, cd):
     assert torch.allclose(sc[0].sum(-1), torch.full((2,), 4.0, device="cuda"), atol=1e-4)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("dt,cd", [("bf16", "bf16"), ("f16", "int8")])
+def test_decode_wait_that_runs_out(pa, dt, cd, wide):
+    """A stage that never arrives: the bounded wait ends, the error is reported, and the
+    next call is right again (the workspace needs no clearing)."""
+    b = Batch(dt, cd, [90, 200], [1, 1], 8, 2, 128, 16, 19)
+    if wide:
+        _wide(b)
+    g = b.gpu()
+    ws = pa.MaskedWorkspace(2, 8, 2, 128, 200)
+    sc = torch.zeros((2, 2, 200), device="cuda")
+    try:
+        pa.set_fault_injection(1)
+        pa.set_wait_limit_ns(1_000_000)
+        _decode(pa, b, g, scores_out=sc, workspace=ws)
+        torch.cuda.synchronize()
+        assert pa.get_device_error(clear=True) & pa.DEVERR_TIMEOUT
+    finally:
+        pa.set_fault_injection(0)
+        pa.set_wait_limit_ns(0)
+    _close(_decode(pa, b, g, scores_out=sc, workspace=ws), b)
+    assert pa.get_device_error(clear=True) == 0
+
+
+@pytest.mark.gpu
+def test_empty_batches(pa):
+    b = Batch("f16", "f16", [20], [1], 8, 2, 128, 16, 1)
+    g = b.gpu()
+    none = dict(q=g["q"][:0], kv=g["kv"], sc=g["sc"], table=g["table"][:0], lens=g["lens"][:0],
+                begin=g["begin"][:1], slopes=None, starts=None, prefix=None)
+    assert _decode(pa, b, none).shape == (0, 8, 128)
+    assert _prefill(pa, b, none).shape == (0, 8, 128)
+    kept, lens, sc = pa.evict(*g["kv"], g["table"][:0], g["lens"][:0], g["table"][:0],
+                              torch.zeros((0, 2, 20), device="cuda"), 8, 2)
+    assert kept.shape == (0, 2, 8) and lens.shape == (0,)
+
+
+@pytest.mark.gpu
+def test_workspaces_that_are_too_small_are_refused(pa):
+    b = Batch("f16", "f16", [20, 30], [1, 1], 8, 2, 128, 16, 1)
+    sc = torch.zeros((2, 2, 30), device="cuda")
+    with pytest.raises(pa.PAError) as e:
+        _decode(pa, b, scores_out=sc, workspace=pa.MaskedWorkspace(2, 8, 2, 128, 29))
+    assert e.value.status == pa.PA_ERR_INVALID_ARG
+    with pytest.raises(ValueError, match="contiguous"):
+        _decode(pa, b, dict(b.gpu(), q=b.q.cuda().transpose(0, 1).contiguous().transpose(0, 1)))
+
+
 # ---------------------------------------------------------------------- prefill
 
 PFORMS = dict(FORMS, docs=dict(), prefix=dict(softcap=15.0), mixed=dict(alibi=True, window=90))
@@ -453,6 +502,25 @@ def test_prefill_query_rows_past_the_batch_are_skipped(pa):
     assert int(flag) == pa.DEVERR_SEQ_LEN
     pa.get_device_error(clear=True)
     assert torch.equal(out[:16], good[:16]) and (out[16:] == 3.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_prefill_wait_that_runs_out(pa, dt):
+    b = Batch(dt, dt, [300, 90], [140, 20], 8, 2, 128, 16, 19, softcap=9.0)
+    g = b.gpu()
+    try:
+        pa.set_fault_injection(1)
+        pa.set_wait_limit_ns(1_000_000)
+        out = _prefill(pa, b, g)
+        torch.cuda.synchronize()
+        assert pa.get_device_error(clear=True) & pa.DEVERR_TIMEOUT
+        assert not out.any()                               # abandoned tiles write zeros
+    finally:
+        pa.set_fault_injection(0)
+        pa.set_wait_limit_ns(0)
+    _close(_prefill(pa, b, g), b)
+    assert pa.get_device_error(clear=True) == 0
 
 
 @pytest.mark.gpu
