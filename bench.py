@@ -57,8 +57,9 @@ NOMINAL_HBM_GBS = 8000.0
 DEFAULT_ALSO = "long_ctx_bf16,long_ctx_bf16@v2,quant_int8,quant_fp8,mixed_f16"
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "decode_traffic.json")
 KERNEL_SOURCES = [os.path.join(ROOT, "paged_kv_cache_390_b200", "csrc", f)
-                  for f in ("pa_decode.cu", "pa_fused.cu", "pa_tile.cuh", "pa_device.cuh",
-                            "pa_write.cuh", "pa_internal.h", "pa_api.cu")]
+                  for f in ("pa_decode.cu", "pa_decode_kernel.cuh", "pa_fused.cu",
+                            "pa_fused_kernel.cuh", "pa_score.cuh", "pa_tile.cuh",
+                            "pa_device.cuh", "pa_write.cuh", "pa_internal.h", "pa_api.cu")]
 STEP_DECODE = {"append": "append_decode_v1 (the new token's cache write fused into the v1 "
                          "decode: one launch)",
                "cascade": "decode_cascade (the shared prefix on tcgen05 once per kv head, beside "

@@ -286,7 +286,8 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
  *   out[s, h, :] = sum_t softmax_t(x_t) V_t
  * over the tokens it sees, max(kv_start[s], pos - window + 1) <= t <= pos.
  *
- *   softcap        > 0 and not below 2^-20 |scale|, or 0: x_t = scale * q . K_t - ...
+ *   softcap        > 0 with softcap / |scale| in [2^-20, 2^60], or 0: x_t =
+ *                  scale * q . K_t - ...
  *   alibi_slopes   fp32 [num_heads] (finite) or NULL: no bias.
  *   kv_start       int32 [num_seqs] or NULL (0): the first token of the new token's
  *                  document.  Values below 0 count as 0; at or past seq_lens[s] the

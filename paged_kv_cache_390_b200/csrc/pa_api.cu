@@ -637,7 +637,10 @@ namespace {
 int check_scores(float scale, float softcap, const float* slopes, const int32_t* kv_start,
                  int window) {
   if (!std::isfinite(softcap) || softcap < 0.f || window < 0) return PA_ERR_INVALID_ARG;
-  if (softcap > 0.f && softcap < std::fabs(scale) * 0x1p-20f) return PA_ERR_INVALID_ARG;
+  if (softcap > 0.f && scale != 0.f) {     // scale / softcap stays a normal number
+    const float ratio = softcap / std::fabs(scale);
+    if (!(ratio >= 0x1p-20f && ratio <= 0x1p60f)) return PA_ERR_INVALID_ARG;
+  }
   if (!aligned(slopes, 4) || !aligned(kv_start, 4)) return PA_ERR_INVALID_ARG;
   return PA_OK;
 }

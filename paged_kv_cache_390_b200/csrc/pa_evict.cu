@@ -14,9 +14,10 @@
 // run of the tokens, its keys read once into shared memory, and the CTAs add up their
 // digit counts through distributed shared memory; then the cluster's threads copy the
 // kept rows, 16 bytes a thread, eight rows' loads before their stores.  Bound: the rows'
-// bytes once the selection (~8 us) is done.  (The first form, one CTA per (sequence, kv
-// head) and a second launch to move, spent 100 of its 144 us on the large case counting
-// digits on 64 of the SMs.)
+// bytes once the tokens are selected.  8 x 16k tokens to 4096, 8 kv heads, bf16 (275 MB):
+// 68 us, of them ~45 at 6.2 TB/s for the rows and ~18 for the selection (four digits at
+// ~2 us, the scores' load, the places); 16 x 640 to 256: 16 us.  (The first form, one CTA per
+// (sequence, kv head) and a second launch to move, took 144.)
 #include <cooperative_groups.h>
 
 #include "pa_device.cuh"

@@ -5,9 +5,17 @@
 //   lo = max(kv_start, pos - window + 1),  hi = min(len, max(pos + 1, prefix_len)),
 //   out = softmax(x) V; a row that sees nothing gets zeros.
 // pa_decode_masked also adds each cached token's weight, summed over the query heads of
-// its kv head, to a running score: the attention leaves its scores x in the workspace
-// and log-sum-exps beside them, and a second launch turns them into weights, so K is not
-// read twice.
+// its kv head, to a running score: the attention leaves its scores x in the workspace and
+// they come back as weights once the log-sum-exps are known, so K is not read twice (32
+// bytes a token and kv head at 8 query heads, against 512 of K and V at 16 bits).
+//
+// Here: the CUDA-core form (fp32 caches; prefills that the tcgen05 kernel does not take),
+// the second launch of the persistent decode, and the choice of form.  The tensor-core
+// forms are the MASK builds of pa_decode_kernel.cuh and pa_fused_kernel.cuh and the MOD
+// builds of pa_prefill_kernel.cuh.  Decode is bound by the cache's bytes: 8 x 32k tokens,
+// bf16, with scores (1.04 GB) 213 us, 172 of them in the attention launch (6.0 TB/s);
+// 32 x 640, fp16, capped (85 MB) 18.4 us; 64 windows of 4096, FP8 (552 MB) 145 us, there
+// by the widening of the codes (ALU pipe 58% busy).
 #include "pa_decode_kernel.cuh"
 #include "pa_fused_kernel.cuh"
 #include "pa_write.cuh"

@@ -267,6 +267,20 @@ def test_decode_bf16_range_over_8_bit_caches(pa, cd, kv, qm, wide):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+@pytest.mark.parametrize("form", ["plain", "cap", "alibi", "all"])
+def test_negative_and_zero_scales(pa, form, scale):
+    for dt, cd in (("bf16", "bf16"), ("f16", "int8"), ("f32", "f32")):
+        b = Batch(dt, cd, [200, 33], [1, 1], 8, 2, 64, 16, 23, **FORMS[form])
+        b.scale = scale
+        _close(_decode(pa, b), b, "decode")
+    for dt in ("f16", "bf16"):
+        b = Batch(dt, dt, [200, 33], [150, 20], 8, 2, 128, 16, 24, **FORMS[form])
+        b.scale = scale
+        _close(_prefill(pa, b), b, "prefill")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_prefill_large_logits_and_steep_biases(pa, dt):
     """Scores past the polynomial's range (tanh over its whole range), and a slope so
@@ -647,6 +661,7 @@ def _cdecode(lib, **over):
 @pytest.mark.parametrize("over,status", [
     (dict(S=0), 0), (dict(S=0, cap=-1.0), 1), (dict(S=0, window=0, win=-1), 1),
     (dict(S=0, cap=float("inf")), 1), (dict(S=0, cap=float("nan")), 1), (dict(S=0, cap=1e-9), 1),
+    (dict(S=0, cap=1e30), 1), (dict(S=0, cap=1e30, scale=0.0), 0),
     (dict(q=None), 1), (dict(D=96), 2), (dict(H=18, Hkv=2), 2), (dict(cd=3), 1), (dict(ws=None), 1),
     (dict(ws=ctypes.c_void_p((1 << 20) + 16)), 1), (dict(wsb=100), 1),
     (dict(si=ctypes.c_void_p(1 << 20)), 1), (dict(so=ctypes.c_void_p(1 << 20)), 1),
