@@ -377,20 +377,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
   if constexpr (MASK) {
     if (!a.scores_out || bad) return;             // a skipped sequence keeps its scores
     __shared__ float lse[kMaxGroup];
-    if (threadIdx.x < G) {
+    if (threadIdx.x < kMaxGroup) {
       float M = -INFINITY, L = 0.f;
       for (int w = 0; w < nwarps; ++w) M = fmaxf(M, mred[w * 8 + threadIdx.x]);
       if (M != -INFINITY)
         for (int w = 0; w < nwarps; ++w)
           L += lred[w * 8 + threadIdx.x] * fast_exp2(mred[w * 8 + threadIdx.x] - M);
-      lse[threadIdx.x] = L > 0.f ? M + log2f(L) : -INFINITY;
+      lse[threadIdx.x] = threadIdx.x < G ? weight_lse(M, L) : INFINITY;
     }
     __syncthreads();                              // the scores x are this CTA's own writes
-    const float* x = a.logits + unit * a.score_stride * G;
     for (int t = threadIdx.x; t < min(len, a.score_stride); t += blockDim.x) {
       const size_t i = unit * a.score_stride + t;
       const float before = a.scores_in ? a.scores_in[i] : 0.f;
-      a.scores_out[i] = before + (t >= lo ? token_weight(x + static_cast<size_t>(t) * G, lse, G) : 0.f);
+      float x[8];
+      load_scores(a.logits + i * G, t >= lo, G, x);
+      a.scores_out[i] = before + token_weight(x, lse);
     }
   }
 }

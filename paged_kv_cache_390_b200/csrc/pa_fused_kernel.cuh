@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
       emit(outp, sc0, sc1);
       if constexpr (MASK) {
         if (a.lse && r == 0) {
-          if (g0ok) a.lse[prow + 2 * c] = l0 > 0.f ? wa.m2[0] + log2f(l0) : -INFINITY;
-          if (g1ok) a.lse[prow + 2 * c + 1] = l1 > 0.f ? wa.m2[1] + log2f(l1) : -INFINITY;
+          if (g0ok) a.lse[prow + 2 * c] = weight_lse(wa.m2[0], l0);
+          if (g1ok) a.lse[prow + 2 * c + 1] = weight_lse(wa.m2[1], l1);
         }
       }
       __syncwarp();

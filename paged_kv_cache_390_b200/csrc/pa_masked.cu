@@ -136,19 +136,21 @@ __global__ void __launch_bounds__(256)
         static_cast<__nv_bfloat16*>(a.out)[qrow + lane + 32 * e] = __float2bfloat16_rn(o);
     }
     if (a.lse && lane == 0)
-      a.lse[static_cast<size_t>(s) * a.num_heads + h] = l == 0.f ? -INFINITY : m2 + log2f(l);
+      a.lse[static_cast<size_t>(s) * a.num_heads + h] = weight_lse(m2, l);
   }
 }
 
 // After the persistent form, per (sequence, kv head): CTA x = 0 merges the unit's records
 // by log-sum-exp into out (a unit that one warp had to itself is already there), the
 // others add the weights to the running scores, kTokens cached tokens each, from
-// log-sum-exps that every CTA takes from the records' (m, l) for itself.
+// log-sum-exps that every CTA takes from the records' (m, l) for itself.  That takes five
+// loads one after another, so a CTA has many tokens and four fit an SM (1024 tokens, two
+// per SM: 37 us for 8 x 32k tokens).
 // One warp per query head of the kv head; a merge keeps 8 records' loads in flight.
-constexpr int kFinish = 256, kTokens = 1024;
+constexpr int kFinish = 256, kTokens = 4096;
 
 template <typename QT, int D>
-__global__ void __launch_bounds__(kFinish)
+__global__ void __launch_bounds__(kFinish, 4)
     masked_finish_kernel(const __grid_constant__ MaskedArgs a, const int* __restrict__ prefix,
                          const float* __restrict__ records, int warps) {
   constexpr uint32_t FULL = 0xffffffffu;
@@ -160,20 +162,45 @@ __global__ void __launch_bounds__(kFinish)
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int G = a.num_heads / a.num_kv_heads;
   const size_t row = static_cast<size_t>(s) * a.num_heads + kvh * G + g;
-  const long long total = prefix[a.num_seqs], W = masked_warps_used(total, warps);
-  const int c0 = prefix[s], nt = (prefix[s + 1] - c0) / a.num_kv_heads;
-  const long long q = total / W, rem = total % W;
-  auto range_start = [&](long long w) { return w * q + (w < rem ? w : rem); };
-  auto warp_of = [&](long long t) {
+  // the split of pa_fused_kernel.cuh, in 32 bits (fewer than 2^31 tiles): its 64-bit
+  // divisions, in every CTA here, were a third of this launch
+  const unsigned total = prefix[a.num_seqs];
+  const unsigned W = static_cast<unsigned>(masked_warps_used(total, warps));
+  const unsigned c0 = prefix[s], nt = (prefix[s + 1] - c0) / a.num_kv_heads;
+  const unsigned q = total / W, rem = total - q * W;
+  auto range_start = [&](unsigned w) { return w * q + min(w, rem); };
+  auto warp_of = [&](unsigned t) {
     return t < (q + 1) * rem ? t / (q + 1) : rem + (t - (q + 1) * rem) / q;
   };
-  const long long start = c0 + static_cast<long long>(kvh) * nt;
-  const long long wf = nt > 0 ? warp_of(start) : 0, wl = nt > 0 ? warp_of(start + nt - 1) : 0;
+  const unsigned start = c0 + kvh * nt;
+  const unsigned wf = nt > 0 ? warp_of(start) : 0, wl = nt > 0 ? warp_of(start + nt - 1) : 0;
   const int n = nt > 0 ? static_cast<int>(wl - wf + 1) : 0;      // records (1: none was left)
   const int slot_f = nt > 0 && range_start(wf) == start ? 0 : 1;
   auto record = [&](int t) {
     return records + static_cast<size_t>(2 * (wf + t) + (t == 0 ? slot_f : 0)) * REC;
   };
+  // a score CTA's own loads first: they do not depend on the log-sum-exps
+  const int len = a.seq_lens[s];
+  const bool bad = len < 0 ||
+                   static_cast<long long>(len) > static_cast<long long>(a.max_blocks) * a.block_size;
+  const int lo = seen_span(a.kv_start ? a.kv_start[s] : 0, len - 1, a.window, 0, len).lo;
+  const int have = min(len, a.score_stride);
+  const int from = (static_cast<int>(blockIdx.x) - 1) * kTokens;
+  const size_t unit = (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride;
+  constexpr int NT = 2;                           // tokens a thread has in flight
+  float x[NT][kMaxGroup], before[NT];
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int t = t0 + u * kFinish + threadIdx.x;
+      before[u] = t < have && a.scores_in ? a.scores_in[unit + t] : 0.f;
+      load_scores(a.logits + (unit + t) * G, t >= lo && t < have, G, x[u]);
+    }
+  };
+  if (blockIdx.x > 0) {
+    if (bad || from >= have) return;              // a skipped sequence keeps its scores
+    load(from);
+  }
   float M = -INFINITY, L = 0.f;
   if (n > 1 && g < G) {
     for (int t = lane; t < n; t += 32) M = fmaxf(M, record(t)[8 * D + g]);
@@ -224,23 +251,19 @@ __global__ void __launch_bounds__(kFinish)
     }
     return;
   }
-  const int len = a.seq_lens[s];
-  if (len < 0 || static_cast<long long>(len) > static_cast<long long>(a.max_blocks) * a.block_size)
-    return;                                       // a skipped sequence keeps its scores
-  const int have = min(len, a.score_stride), from = (blockIdx.x - 1) * kTokens;
-  if (from >= have) return;
-  if (g < G && lane == 0)
-    lse[g] = n == 1 ? a.lse[row] : (L > 0.f ? M + log2f(L) : -INFINITY);
+  if (lane == 0) lse[g] = g >= G ? INFINITY : (n == 1 ? a.lse[row] : weight_lse(M, L));
   __syncthreads();
-  const int lo = seen_span(a.kv_start ? a.kv_start[s] : 0, len - 1, a.window, 0, len).lo;
-  const size_t unit = (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride;
+  const int end = min(have, from + kTokens);
+  for (int t0 = from; t0 < end; t0 += NT * kFinish) {
+    float sum[NT];
 #pragma unroll
-  for (int u = 0; u < kTokens / kFinish; ++u) {
-    const int t = from + u * kFinish + threadIdx.x;
-    if (t >= have) break;
-    const float before = a.scores_in ? a.scores_in[unit + t] : 0.f;
-    a.scores_out[unit + t] =
-        before + (t >= lo ? token_weight(a.logits + (unit + t) * G, lse, G) : 0.f);
+    for (int u = 0; u < NT; ++u) sum[u] = before[u] + token_weight(x[u], lse);
+    if (t0 + NT * kFinish < end) load(t0 + NT * kFinish);
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      const int t = t0 + u * kFinish + threadIdx.x;
+      if (t < have) a.scores_out[unit + t] = sum[u];
+    }
   }
 }
 
@@ -257,15 +280,19 @@ __global__ void __launch_bounds__(256)
   const int n = min(len, a.score_stride);
   if (blockIdx.x * 256 >= n) return;
   const int G = a.num_heads / a.num_kv_heads;
-  if (threadIdx.x < G)
-    lse[threadIdx.x] = a.lse[static_cast<size_t>(s) * a.num_heads + kvh * G + threadIdx.x];
+  if (threadIdx.x < kMaxGroup)
+    lse[threadIdx.x] = threadIdx.x < G
+                           ? a.lse[static_cast<size_t>(s) * a.num_heads + kvh * G + threadIdx.x]
+                           : INFINITY;
   __syncthreads();
   const int t = blockIdx.x * 256 + threadIdx.x;
   if (t >= n) return;
   const Span sp = seen_span(a.kv_start ? a.kv_start[s] : 0, len - 1, a.window, 0, len);
   const size_t i = (static_cast<size_t>(s) * a.num_kv_heads + kvh) * a.score_stride + t;
   const float before = a.scores_in ? a.scores_in[i] : 0.f;
-  a.scores_out[i] = before + (t >= sp.lo ? token_weight(a.logits + i * G, lse, G) : 0.f);
+  float x[kMaxGroup];
+  load_scores(a.logits + i * G, t >= sp.lo, G, x);
+  a.scores_out[i] = before + token_weight(x, lse);
 }
 
 template <typename QT, typename KT>

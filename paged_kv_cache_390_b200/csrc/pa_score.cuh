@@ -51,20 +51,39 @@ __host__ __device__ __forceinline__ long long masked_warps_used(long long tiles,
   return most < 1 ? 1 : (most < warps ? most : warps);
 }
 
-// A cached token's weight summed over the G query heads of its kv head, from their scores
-// x and log-sum-exps (log2 units; -inf: that head's row saw nothing).
-__device__ __forceinline__ float token_weight(const float* x, const float* lse, int G) {
-  float w = 0.f;
+// A cached token's scores x under the G (up to 8) query heads of its kv head, log2 units;
+// -inf where it is not seen.
+__device__ __forceinline__ void load_scores(const float* p, bool seen, int G, float (&x)[8]) {
   if ((G & 3) == 0) {
-    for (int g = 0; g < G; g += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(x + g);
-      w += (lse[g] != -INFINITY ? exp2f(v.x - lse[g]) : 0.f) +
-           (lse[g + 1] != -INFINITY ? exp2f(v.y - lse[g + 1]) : 0.f) +
-           (lse[g + 2] != -INFINITY ? exp2f(v.z - lse[g + 2]) : 0.f) +
-           (lse[g + 3] != -INFINITY ? exp2f(v.w - lse[g + 3]) : 0.f);
+#pragma unroll
+    for (int g = 0; g < 8; g += 4) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (seen && g < G) v = *reinterpret_cast<const float4*>(p + g);
+      x[g] = v.x;
+      x[g + 1] = v.y;
+      x[g + 2] = v.z;
+      x[g + 3] = v.w;
     }
   } else {
-    for (int g = 0; g < G; ++g) w += lse[g] != -INFINITY ? exp2f(x[g] - lse[g]) : 0.f;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) x[g] = seen && g < G ? p[g] : -INFINITY;
+  }
+}
+
+// A head's log-sum-exp (log2 units) from its maximum and sum; +inf, which makes every
+// weight 0, where its row saw nothing.
+__device__ __forceinline__ float weight_lse(float M, float L) {
+  return L > 0.f || L != L ? M + log2f(L) : INFINITY;
+}
+
+// A token's weight, summed over the heads (lse: 8 of them, +inf past G).
+__device__ __forceinline__ float token_weight(const float (&x)[8], const float* lse) {
+  float w = 0.f;
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(x[g] - lse[g]));
+    w += p;
   }
   return w;
 }

@@ -274,7 +274,7 @@ def rope_and_cache(q, key, value, positions, inv_freq, pair_axis, k_cache, v_cac
     ctx = _enter(index, stream)
     try:
         if out is None:
-            out = torch.empty((num_tokens, num_heads, head_dim), dtype=dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         rc = (_lib or lib()).pa_rope_and_cache(
             out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), _FLOAT_CODES[dtype],
             *strides, positions.data_ptr(), num_axes, inv_freq.data_ptr(), pair_axis.data_ptr(),
