@@ -231,6 +231,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n = min(end - base, kKeys / 2);
     for (int i = tid; i < n; i += kThreads) {
       const int j = base + i, t = __ldcg(kept + j);
+      if (t < 0 || t >= len) {                 // a place left open by scores that changed
+        moves[i] = make_int2(-1, -1);
+        continue;
+      }
       const int sb = stab[t >> bsh], db = dtab[j >> bsh];
       if (nsc) nsc[j] = sc[t];
       const bool ok = sb >= 0 && sb < a.num_blocks && db >= 0 && db < a.num_blocks;
