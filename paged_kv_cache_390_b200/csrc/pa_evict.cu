@@ -4,8 +4,9 @@
 //
 // Which tokens stay is a selection of the r-th largest of up to max_blocks * block_size
 // fp32 scores (r = num_keep - num_recent): scores become unsigned keys of the same
-// order, and four passes of 8 bits count digits in shared memory and narrow the
-// threshold's digits, most significant first.  Tokens above the threshold stay, and of
+// order, and up to four passes of 8 bits count digits in shared memory and narrow the
+// threshold's digits, most significant first, until all the keys that begin with them
+// stay (spread scores: mostly after two or three).  Tokens above the threshold stay, and of
 // those equal to it the first ones until r are found; a token's place is the number of
 // tokens before it that are above the threshold plus that of equal ones, as far as they
 // stay.  Whole-number counts, so the same tokens every time.
@@ -15,8 +16,8 @@
 // digit counts through distributed shared memory; then the cluster's threads copy the
 // kept rows, 16 bytes a thread, eight rows' loads before their stores.  Bound: the rows'
 // bytes once the tokens are selected.  8 x 16k tokens to 4096, 8 kv heads, bf16 (275 MB):
-// 68 us, of them ~45 at 6.2 TB/s for the rows and ~18 for the selection (four digits at
-// ~2 us, the scores' load, the places); 16 x 640 to 256: 16 us.  (The first form, one CTA per
+// 66 us, of them ~45 at 6.2 TB/s for the rows and ~16 for the selection (the scores' load,
+// digits at ~2 us, the places); 16 x 640 to 256: 14.2 us, ~7 for the rows.  (The first form, one CTA per
 // (sequence, kv head) and a second launch to move, took 144.)
 #include <cooperative_groups.h>
 
@@ -42,6 +43,10 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // Sequence length if its tokens lie inside the table and the scores and what stays
 // fits the new table and the outputs, else -1 (always checked).
 __device__ __forceinline__ int checked_len(const EvictArgs& a, int s) {
@@ -55,19 +60,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     evict_kernel(const __grid_constant__ EvictArgs a) {
   constexpr uint32_t FULL = 0xffffffffu;
   __shared__ __align__(8) uint32_t keys[kKeys];
-  // Digit counts of this CTA, the highest digit first.  Three in turn: pass p fills one and clears the next, which
-  // was last read in pass p - 2, so before everybody came to pass p - 1's barrier.
+  // Digit counts of this CTA, the highest digit first.  Three in turn: pass p fills one
+  // and clears the next, which was last read in pass p - 2, so before everybody came to
+  // pass p - 1's barrier.
   __shared__ __align__(16) uint32_t hist[3][256];
-  __shared__ __align__(16) uint32_t total[256];   // of the cluster
+  __shared__ uint32_t found[3];                // threshold so far, keys wanted of it, its keys
   __shared__ uint32_t counts[2];               // this CTA's keys above / equal to the threshold
   __shared__ uint32_t wcount[2][kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = blockIdx.x, nc = gridDim.x, kvh = blockIdx.y, s = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
+  if (tid < 256) hist[0][tid] = 0;
+  __syncthreads();
   griddep_wait();
-  const int len = checked_len(a, s);
   const size_t unit = static_cast<size_t>(s) * a.num_kv_heads + kvh;
+  const float* sc = a.scores + unit * a.score_stride;
+  const int32_t* stab = a.src_tables + static_cast<size_t>(s) * a.max_src_blocks;
+  const int32_t* dtab = a.dst_tables + static_cast<size_t>(s) * a.max_dst_blocks;
+  // the first scores and table entries come while the length does
+  if (nc == 1 && tid < 128 && 32 * tid < a.score_stride) prefetch_l1(sc + 32 * tid);
+  if (warp < kWarps / 2) {
+    if (32 * tid < a.max_src_blocks) prefetch_l1(stab + 32 * tid);
+  } else if (32 * (tid - kThreads / 2) < a.max_dst_blocks) {
+    prefetch_l1(dtab + 32 * (tid - kThreads / 2));
+  }
+  const int len = checked_len(a, s);
   int* kept = a.kept + unit * a.kept_stride;
   if (len < 0) {                               // skipped (the whole cluster): nothing kept
     if (tid == 0 && kvh == 0 && rank == 0) {
@@ -77,7 +95,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = rank * kThreads + tid; i < a.kept_stride; i += nc * kThreads) kept[i] = -1;
     return;
   }
-  const float* sc = a.scores + unit * a.score_stride;
   float* nsc = a.new_scores ? a.new_scores + unit * a.new_score_stride : nullptr;
   const int m = min(len, a.num_keep);
   const int old = max(0, len - a.num_recent);  // tokens that compete by score
@@ -96,68 +113,85 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int run = per_warp * kWarps;
     const int t_lo = min(old, rank * run), t_hi = min(old, t_lo + run);
     const bool held = run <= kKeys;
-    if (held)
-      for (int t = t_lo + tid; t < t_hi; t += kThreads) keys[t - t_lo] = score_key(sc[t]);
     auto key = [&](int t) { return held ? keys[t - t_lo] : score_key(sc[t]); };
-    if (tid < 256) hist[0][tid] = 0;
-    __syncthreads();
+    // Keys, and the first digit on the way: sign and exponent, so a warp's keys share a few
+    // digits and equal ones are counted by one lane (32 lanes on one counter take 32 turns).
+    // Four loads of a thread in flight.
+#pragma unroll 1
+    for (int t0 = t_lo + tid; t0 < t_hi; t0 += 4 * kThreads) {
+      float x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (t0 + u * kThreads < t_hi) x[u] = sc[t0 + u * kThreads];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = t0 + u * kThreads;
+        if (t >= t_hi) break;
+        const uint32_t k = score_key(x[u]);
+        if (held) keys[t - t_lo] = k;
+        const uint32_t d = 255u - (k >> 24);
+        const uint32_t same = __match_any_sync(__activemask(), d);
+        if (lane == __ffs(same) - 1) atomicAdd(&hist[0][d], __popc(same));
+      }
+    }
     uint32_t thr = 0, mask = 0, want = static_cast<uint32_t>(r);
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass, buf = pass % 3;
       if (tid < 256) hist[(pass + 1) % 3][tid] = 0;
-      if (pass == 0) {
-        // sign and exponent: a warp's keys share a few digits, so equal ones are counted
-        // by one lane (32 lanes on one counter take 32 turns)
-        for (int t = t_lo + tid; t < t_hi; t += kThreads) {
-          const uint32_t d = 255u - (key(t) >> 24);
-          const uint32_t same = __match_any_sync(__activemask(), d);
-          if (lane == __ffs(same) - 1) atomicAdd(&hist[0][d], __popc(same));
-        }
-      } else {
+      if (pass > 0) {
         for (int t = t_lo + tid; t < t_hi; t += kThreads) {
           const uint32_t k = key(t);
           if ((k & mask) == thr) atomicAdd(&hist[buf][255u - ((k >> shift) & 255u)], 1u);
         }
       }
       sync();
-      const uint32_t* sum_of = hist[buf];
-      if (nc > 1) {
-        if (tid < 256) {
-          uint32_t sum = 0;
+      // Warp 0 finds the digit; lane l holds digits 255 - 8l .. 248 - 8l.
+      if (warp == 0) {
+        uint32_t c[8] = {};
 #pragma unroll
-          for (int c = 0; c < kMaxCluster; ++c)
-            if (c < nc) sum += cluster.map_shared_rank(&hist[buf][0], c)[tid];
-          total[tid] = sum;
+        for (int cta = 0; cta < kMaxCluster; ++cta) {
+          if (cta < nc) {
+            const uint32_t* from = nc > 1 ? cluster.map_shared_rank(&hist[buf][0], cta) : hist[buf];
+            const uint4 c0 = reinterpret_cast<const uint4*>(from)[2 * lane];
+            const uint4 c1 = reinterpret_cast<const uint4*>(from)[2 * lane + 1];
+            c[0] += c0.x; c[1] += c0.y; c[2] += c0.z; c[3] += c0.w;
+            c[4] += c1.x; c[5] += c1.y; c[6] += c1.z; c[7] += c1.w;
+          }
         }
-        __syncthreads();
-        sum_of = total;
-      }
-      // every warp finds the digit for itself; lane l: digits 255 - 8l .. 248 - 8l
-      const uint4 c0 = reinterpret_cast<const uint4*>(sum_of)[2 * lane];
-      const uint4 c1 = reinterpret_cast<const uint4*>(sum_of)[2 * lane + 1];
-      const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-      const uint32_t sum = c0.x + c0.y + c0.z + c0.w + c1.x + c1.y + c1.z + c1.w;
-      uint32_t incl = sum;
+        uint32_t sum = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl += v;
-      }
-      uint32_t before = incl - sum, digit = 0, inside = 0;
-      const bool mine = before < want && incl >= want;
+        for (int i = 0; i < 8; ++i) sum += c[i];
+        uint32_t incl = sum;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (mine && before < want && before + c[i] >= want) {
-          digit = 255 - 8 * lane - i;
-          inside = want - before;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_up_sync(FULL, incl, o);
+          if (lane >= o) incl += v;
         }
-        before += c[i];
+        uint32_t before = incl - sum;
+        if (before < want && incl >= want) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (before < want && before + c[i] >= want) {
+              found[0] = thr | ((255u - 8 * lane - i) << shift);
+              found[1] = want - before;
+              found[2] = c[i];
+              break;
+            }
+            before += c[i];
+          }
+        }
       }
-      const int src = __ffs(__ballot_sync(FULL, mine)) - 1;
-      thr |= __shfl_sync(FULL, digit, src) << shift;
-      want = __shfl_sync(FULL, inside, src);
+      __syncthreads();
+      thr = found[0];
+      want = found[1];
       mask |= 255u << shift;
+      // everything that begins with these digits stays: they are the threshold (zeros
+      // after them), the further digits do not matter
+      if (found[2] == want) {
+        want = ~0u;
+        break;
+      }
     }
     // `want` of the tokens equal to the threshold stay, the first ones
     const int w_lo = min(t_hi, t_lo + warp * per_warp), w_hi = min(t_hi, w_lo + per_warp);
@@ -222,8 +256,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const size_t pitch = static_cast<size_t>(a.num_kv_heads) * a.row_vecs;
   uint4* pool = static_cast<uint4*>(is_v ? a.v_cache : a.k_cache) +
                 static_cast<size_t>(kvh) * a.row_vecs + (is_v ? v - a.row_vecs : v);
-  const int32_t* stab = a.src_tables + static_cast<size_t>(s) * a.max_src_blocks;
-  const int32_t* dtab = a.dst_tables + static_cast<size_t>(s) * a.max_dst_blocks;
   int2* moves = reinterpret_cast<int2*>(keys);             // (source, destination) slots
   const int per = (m + nc - 1) / nc;
   const int end = min(m, (rank + 1) * per);

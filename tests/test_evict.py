@@ -113,6 +113,27 @@ def test_ties_zeros_infinities_and_nan(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [600, 9000])
+@pytest.mark.parametrize("digit", [0, 1, 2, 3])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_a_digit_that_decides_alone(pa, n, digit, more):
+    """keep - recent + more tokens share the score's first digits (8 bits each) up to
+    `digit` and differ behind it; the others are lower in that digit."""
+    keep, recent, Hkv = 200, 20, 2
+    case = _case([n], Hkv, 64, 16, "f16", keep, 31)
+    g = torch.Generator().manual_seed(1000 * digit + more)
+    top = 0x4B4B4B4B
+    shift = 24 - 8 * digit
+    low = torch.randint(0, 1 << shift, (Hkv, n), generator=g) if shift else torch.zeros(Hkv, n, dtype=torch.long)
+    high = torch.full((Hkv, n), (top >> shift) - 1)
+    for h in range(Hkv):
+        high[h, torch.randperm(n - recent, generator=g)[:keep - recent + more]] += 1
+    case[6][0, :, :n] = ((high << shift) + low).to(torch.int32).view(torch.float32)
+    pools, res = _run(pa, case, [n], keep, recent, "f16")
+    _check(case, [n], keep, recent, pools, res, 16)
+
+
+@pytest.mark.gpu
 def test_wide_outputs_keep_their_tails_and_repeat(pa):
     """Outputs wider than needed: kept is filled with -1, new_scores past the new length
     stays; two runs on one input give the same bits; captured and replayed alike."""
