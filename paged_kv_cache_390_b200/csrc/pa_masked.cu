@@ -506,6 +506,7 @@ cudaError_t launch_decode_masked(const MaskedArgs& a0, int q_dtype, int cache_dt
 
 cudaError_t launch_prefill_masked(const MaskedArgs& a, int q_dtype, int cache_dtype, int head_dim,
                                   int max_query_len, cudaStream_t s) {
+  if (max_query_len > a.total_q) max_query_len = a.total_q;     // longer ones are skipped
   if (head_dim != 128 || cache_dtype != q_dtype || q_dtype == PA_F32)
     return launch_attention(a, q_dtype, cache_dtype, head_dim, max_query_len, s);
   PrefillArgs p{};

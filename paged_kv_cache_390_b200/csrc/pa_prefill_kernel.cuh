@@ -105,6 +105,10 @@ __host__ __device__ constexpr int prefill_threads() { return MOD >= 0 ? kThreads
 // in TMEM (S_A, S_B, P_A, P_B: 64 columns each, O_A, O_B: 128), so that the next step's S
 // can be computed while this one's softmax runs.
 constexpr int kSub = 64;
+// MOD >= 0: the order of the CTAs.  Query tiles go out from the last one on, as a causal
+// row's work grows with its position and a long CTA that starts last runs alone; a group
+// of up to 16 neighbours stays together, for their common K and V in L2.
+constexpr int kTileGroup = 16;
 
 // bf16 keeps 8 significant bits: P goes in as a high and a low bf16 part (two
 // PV products, ~16 bits); fp16's 11 bits need one.  P of 128 tokens takes 64
@@ -256,7 +260,13 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
   __shared__ int abort_flag;
   __shared__ int span_lo[8], span_hi[8];     // MASK: the union of each softmax warp's spans
 
-  const int tile2 = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+  int tile2 = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
+  if constexpr (MASK) {                      // grid (kTileGroup tiles x kv heads, sequences, groups)
+    const int ng = gridDim.x / a.num_kv_heads;
+    kvh = blockIdx.x / ng;
+    seq = blockIdx.y;
+    tile2 = static_cast<int>((gridDim.z - blockIdx.z) * ng - 1 - blockIdx.x % ng);
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.num_heads / a.num_kv_heads;
   const int TQ = kRows / G;
@@ -892,6 +902,9 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
     const float inv = (!dead && l_run > 0.f) ? 1.f / l_run : 0.f;
     const int h = kvh * G + row_me % G;
     const size_t orow_idx = static_cast<size_t>(q0 + tok_me) * a.num_heads + h;
+    // this warp's 32 output rows, 16 chunks of 16 bytes each, in Q's place (every product
+    // that read it is done); chunk c of row r at c ^ (r & 15), free of bank conflicts
+    uint4* stage = reinterpret_cast<uint4*>(smem_raw + (sbase - sraw) + kQOff) + 512 * warp;
     const size_t split_rows = cascade ? static_cast<size_t>(seq) * q_len * a.num_heads : 0;
     if (cascade && row_valid) {
       a.part_m[split_rows + orow_idx] = (dead || empty) ? -INFINITY : m_run;
@@ -920,7 +933,6 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
           dst[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv,
                                v[4 * e + 3] * inv);
       } else {
-        QT* orow = reinterpret_cast<QT*>(a.out) + orow_idx * kD + 32 * i;
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
           uint4 w;
@@ -928,9 +940,27 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
           w.y = pack2<QT>(v[e + 2] * inv, v[e + 3] * inv);
           w.z = pack2<QT>(v[e + 4] * inv, v[e + 5] * inv);
           w.w = pack2<QT>(v[e + 6] * inv, v[e + 7] * inv);
-          *reinterpret_cast<uint4*>(orow + e) = w;
+          if (dead || empty)                 // a copy may still be on its way to shared memory
+            *reinterpret_cast<uint4*>(reinterpret_cast<QT*>(a.out) + orow_idx * kD + 32 * i + e) = w;
+          else
+            stage[16 * lane + ((4 * i + e / 8) ^ (lane & 15))] = w;
         }
       }
+    }
+    if (!cascade && !dead && !empty) {
+      // the warp's rows go out two at a time, 512 bytes a store (a thread per row stores 16
+      // bytes to each of 32 lines: 4k clocks a CTA longer)
+      __syncwarp();
+      const long long mine = row_valid ? static_cast<long long>(orow_idx) : -1;
+#pragma unroll 4
+      for (int r = 0; r < 32; r += 2) {
+        const int src = r + (lane >> 4), ch = lane & 15;
+        const long long to = __shfl_sync(FULL, mine, src);
+        if (to >= 0)
+          reinterpret_cast<uint4*>(static_cast<QT*>(a.out) + to * kD)[ch] =
+              stage[16 * src + (ch ^ (src & 15))];
+      }
+      __syncwarp();
     }
     if constexpr (MASK) {                    // the rows that came out non-finite, once more
       uint32_t again = __ballot_sync(FULL, odd && !dead && row_valid);

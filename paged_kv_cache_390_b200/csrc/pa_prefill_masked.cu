@@ -29,7 +29,9 @@ cudaError_t launch_mod(const PrefillArgs& a, int max_query_len, cudaStream_t str
   e = opt_in_smem(reinterpret_cast<const void*>(kern), kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   const int rows_per_cta = kQTiles * (kRows / G);
-  const dim3 grid((max_query_len + rows_per_cta - 1) / rows_per_cta, a.num_kv_heads, a.num_seqs);
+  const int tiles = (max_query_len + rows_per_cta - 1) / rows_per_cta;
+  const int ng = tiles < kTileGroup ? tiles : kTileGroup;
+  const dim3 grid(ng * a.num_kv_heads, a.num_seqs, (tiles + ng - 1) / ng);
   return launch_kernel(kern, grid, dim3(prefill_threads<MOD>()), kSmemBytes, stream, pdl_mode() != 0, mq, mk, mv,
                        a);
 }
