@@ -242,6 +242,10 @@ __device__ __noinline__ void masked_row(const PrefillArgs& a, const int32_t* tab
   }
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // BSC: tokens per block, 0: a.block_size.
 template <typename QT, int BSC, int MOD = -1>
 __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
@@ -270,6 +274,20 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.num_heads / a.num_kv_heads;
   const int TQ = kRows / G;
+
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  if (tid == kTmaWarp * 32) {
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool from_threads = (i >= kBarPFull && i < kBarPFull + 2) ||
+                                (i >= kBarSFree && i < kBarSFree + 2);
+      mbar_init(bar(i), from_threads ? kRows : 1);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
 
   // Wait first, then release the dependent grid: a kernel launched behind this
   // one may then read whatever the kernels before this one wrote.
@@ -323,25 +341,14 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
 
   const uint32_t sraw = smem_u32(smem_raw);
   const uint32_t sbase = (sraw + 1023u) & ~1023u;
-  auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto q_s = [&](int x) { return sbase + kQOff + static_cast<uint32_t>(x * 2 * kQHalf); };
   auto k_s = [&](int st) { return sbase + kKOff + static_cast<uint32_t>(st * kKvTile); };
   auto v_s = [&](int st) { return sbase + kVOff + static_cast<uint32_t>(st * kKvTile); };
   const int32_t* table = a.block_tables + (cascade ? 0 : static_cast<size_t>(seq) * a.max_blocks);
   volatile int* abort = &abort_flag;
 
-  if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
-      const bool from_threads = (i >= kBarPFull && i < kBarPFull + 2) ||
-                                (i >= kBarSFree && i < kBarSFree + 2);
-      mbar_init(bar(i), from_threads ? kRows : 1);
-    }
-    abort_flag = 0;
-    fence_barrier_init();
-    prefetch_tensormap(&tm_q);
-    prefetch_tensormap(&tm_k);
-    prefetch_tensormap(&tm_v);
-  }
+  // the first table entries come while the spans do
+  if (MASK && warp == kTmaWarp && 32 * lane < a.max_blocks) prefetch_l1(table + 32 * lane);
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&tmem_base_slot), kTmemCols);
     tmem_relinquish();
