@@ -32,13 +32,14 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 }
 
 // Bound: the rows' bytes, each read and written once.  8191 tokens x 80 rows x 128 bf16
-// (336 MB): 61.4 us, 5.5 TB/s.  Two or three rows' loads in flight per lane, or the first
+// (336 MB): 59.2 us, 5.7 TB/s, with ten CTAs an SM (48 registers; nine without the bound 61.4,
+// twelve at 40 registers 61.6; fp32 rows 3.6 us without, 4.0 with it).  Two or three rows' loads in flight per lane, or the first
 // ones before the sine and cosine, were slower (63 to 83 us: fewer CTAs fit an SM).
 // One CTA per (token, slice of its rows).  A row of D elements is D / (2 VE) lanes'
 // work; lane j of a row holds pairs [j VE, (j + 1) VE): its two 16-byte vectors are the
 // halves' vectors j (halves form) or the row's vectors 2j and 2j + 1 (side by side).
 template <typename ST, int MODE, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(ST) == 2 && MODE == kWriteCopy ? 10 : 1)
     rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int VE = 16 / static_cast<int>(sizeof(ST));
   constexpr int LPR = D / (2 * VE);            // lanes per row: 8 (16-bit, D 128) .. 16
