@@ -437,6 +437,16 @@ def test_prefill_head_groups_and_blocks(pa, dt, bs, H, Hkv):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("H,Hkv,most", [(64, 1, None), (32, 2, None), (48, 1, 600), (8, 8, 2**31 - 1)])
+def test_prefill_many_query_tiles(pa, dt, H, Hkv, most):
+    """More query tiles than are kept together in the order of the CTAs, chunks of different
+    lengths, a max_query_len far above them."""
+    b = _prefill_batch(dt, dt, "mixed", H, Hkv, 128, 16, H, lens=(300, 5, 310), q_lens=(290, 3, 77))
+    _close(_prefill(pa, b, max_query_len=most), b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_prefill_rows_that_see_nothing(pa, dt):
     """Documents that start behind their row, a window of one, an empty chunk: zeros."""
     lens, q_lens = [200, 50, 30], [140, 0, 30]
