@@ -61,6 +61,9 @@
 //   exponential already keeps the special-function unit (4 results a clock and SM
 //   quarter: 2048 clocks per 128 tokens of both query tiles) nearly as busy as the
 //   products keep the tensor core (3584); tanh through ex2 and rcp would triple it.
+// * Where few query tiles would leave SMs idle, up to 8 CTAs of a cluster share a query
+//   tile's KV tiles; each leaves O and (m, l) in its shared memory, and the cluster merges
+//   them row by row through distributed shared memory (no workspace, a fixed order).
 // * P goes in as two parts for fp16 too: one part's rounding alone is as large as the
 //   output's.
 // * V rows that no row of the CTA sees are zeroed; a row that comes out non-finite (a
@@ -72,6 +75,7 @@
 // 0.87 to 0.94 ms (clocks under the power cap).
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cudaTypedefs.h>
 
 #include "pa_device.cuh"
@@ -110,6 +114,7 @@ constexpr int kSub = 64;
 // row's work grows with its position and a long CTA that starts last runs alone; a group
 // of up to 16 neighbours stays together, for their common K and V in L2.
 constexpr int kTileGroup = 16;
+constexpr int kMaxSplit = 8;               // MOD >= 0: CTAs that share one query tile's KV tiles
 
 // bf16 keeps 8 significant bits: P goes in as a high and a low bf16 part (two
 // PV products, ~16 bits); fp16's 11 bits need one.  P of 128 tokens takes 64
@@ -266,11 +271,14 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
   __shared__ int span_lo[8], span_hi[8];     // MASK: the union of each softmax warp's spans
 
   int tile2 = blockIdx.x, kvh = blockIdx.y, seq = blockIdx.z;
-  if constexpr (MASK) {                      // grid (kTileGroup tiles x kv heads, sequences, groups)
-    const int ng = gridDim.x / a.num_kv_heads;
-    kvh = blockIdx.x / ng;
+  int nsplit = 1, rank = 0;                  // MASK: CTAs that share the KV tiles of one query tile
+  if constexpr (MASK) {                      // grid (splits x tile group x kv heads, sequences, groups)
+    nsplit = static_cast<int>(cooperative_groups::this_cluster().num_blocks());
+    rank = blockIdx.x % nsplit;
+    const int ng = gridDim.x / (nsplit * a.num_kv_heads), bx = blockIdx.x / nsplit;
+    kvh = bx / ng;
     seq = blockIdx.y;
-    tile2 = static_cast<int>((gridDim.z - blockIdx.z) * ng - 1 - blockIdx.x % ng);
+    tile2 = static_cast<int>((gridDim.z - blockIdx.z) * ng - 1 - bx % ng);
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.num_heads / a.num_kv_heads;
@@ -367,10 +375,15 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
     }
     t_lo = u_lo < u_hi ? u_lo / kBN : 0;
     ntiles = u_lo < u_hi ? (u_hi - 1) / kBN + 1 - t_lo : 0;
+    const int per = (ntiles + nsplit - 1) / nsplit, skip = min(ntiles, rank * per);
+    t_lo += skip;
+    ntiles = min(ntiles - skip, per);
   }
   // MASK: steps [i0, i1) of 64 tokens, counted from the first KV tile
-  const int i0 = MASK ? u_lo / kSub - t_lo * (kBN / kSub) : 0;
-  const int i1 = MASK && ntiles > 0 ? (u_hi - 1) / kSub + 1 - t_lo * (kBN / kSub) : i0;
+  const int i0 = MASK && ntiles > 0 ? max(0, u_lo / kSub - t_lo * (kBN / kSub)) : 0;
+  const int i1 = MASK && ntiles > 0
+                     ? min((u_hi - 1) / kSub + 1 - t_lo * (kBN / kSub), ntiles * (kBN / kSub))
+                     : i0;
   // S_x (f32) and, over it once read, P_x (16-bit pairs per column; bf16's low
   // part in columns 64..127)
   auto t_s = [&](int x) { return tmem + static_cast<uint32_t>((MASK ? kSub : 128) * x); };
@@ -902,7 +915,82 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
   tc_fence_after_sync();
   const bool dead = *abort;
   const bool empty = ntiles == 0;            // an empty split: m = -inf, l = 0, o = 0
-  if (warp < 8) {
+  if (MASK && nsplit > 1) {
+    // ---- the cluster's CTAs share the rows out and merge them from each other's shared
+    // memory: O (not yet divided) in Q's and K's place, (m, l) in V's.  Every product and
+    // copy of this CTA is done, or it is dead and its memory is not read.
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    float4* po = reinterpret_cast<float4*>(smem_raw + (sbase - sraw));      // [256][32], swizzled
+    float2* pml = reinterpret_cast<float2*>(smem_raw + (sbase - sraw) + kVOff);
+    if (warp < 8 && !dead) {
+      pml[tid] = empty ? make_float2(-INFINITY, 0.f) : make_float2(m_run, l_run);
+      if (!empty) {
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v[32];
+          tmem_ld32(t_o(x_me) + lane_off + 32 * i, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            po[32 * tid + ((8 * i + e) ^ lane)] =
+                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+      }
+    }
+    tc_fence_before_sync();
+    cluster.sync();
+    if (warp < 8) {
+      bool lost = false;                     // a CTA whose wait ran out: zeros
+      for (int c = 0; c < nsplit; ++c) lost = lost || *cluster.map_shared_rank(&abort_flag, c) != 0;
+      const int share = kQTiles * kRows / nsplit;
+      for (int row = rank * share + warp; row < (rank + 1) * share; row += 8) {
+        const int r = (row % kRows) / G, tok = row0 + row / kRows * TQ + r;
+        if (r >= TQ || tok >= q_len) continue;
+        float m = -INFINITY, l = 0.f;
+        if (lane < nsplit && !lost) {
+          const float2 ml = cluster.map_shared_rank(pml, lane)[row];
+          m = ml.x;
+          l = ml.y;
+        }
+        float M = l == 0.f ? -INFINITY : m;
+#pragma unroll
+        for (int o = kMaxSplit / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+        const float w = l == 0.f || M == -INFINITY ? 0.f : fast_exp2(m - M);
+        float sum = w * l;
+#pragma unroll
+        for (int o = kMaxSplit / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < nsplit; ++c) {
+          const float wc = __shfl_sync(FULL, w, c);
+          if (wc == 0.f) continue;           // nothing seen there: its O is not read
+          const float4 v = cluster.map_shared_rank(po, c)[32 * row + (lane ^ (row & 31))];
+          acc.x = fmaf(wc, v.x, acc.x);
+          acc.y = fmaf(wc, v.y, acc.y);
+          acc.z = fmaf(wc, v.z, acc.z);
+          acc.w = fmaf(wc, v.w, acc.w);
+        }
+        sum = __shfl_sync(FULL, sum, 0);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int pos = L - q_len + tok, h = kvh * G + row % kRows % G;
+        const Span sp = seen_span(a.kv_start ? a.kv_start[q0 + tok] : 0, pos, a.window,
+                                  a.prefix_lens ? a.prefix_lens[seq] : 0, L);
+        const float s = fmaf(0.f, acc.x, fmaf(0.f, acc.y, fmaf(0.f, acc.z, 0.f * acc.w)));
+        const bool odd = !(s == 0.f) || !(sum < INFINITY) || (sp.lo < sp.hi && !(sum > 0.f));
+        if (__any_sync(FULL, odd) && !lost) {
+          masked_row<QT>(a, table, q0 + tok, h, kvh, pos, sp.lo, sp.hi);
+          continue;
+        }
+        uint2 pk;
+        pk.x = pack2<QT>(acc.x * inv, acc.y * inv);
+        pk.y = pack2<QT>(acc.z * inv, acc.w * inv);
+        reinterpret_cast<uint2*>(static_cast<QT*>(a.out) +
+                                 (static_cast<size_t>(q0 + tok) * a.num_heads + h) * kD)[lane] = pk;
+      }
+    }
+    cluster.sync();                          // nobody reads this CTA's memory any more
+  } else if (warp < 8) {
     // ---- epilogue: out row = O / l (cascade: the partial o / l, m, l)
     const int x = x_me;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;

@@ -447,6 +447,60 @@ def test_prefill_many_query_tiles(pa, dt, H, Hkv, most):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("form", sorted(PFORMS))
+@pytest.mark.parametrize("lens,q_lens", [((1500,), (20,)), ((2300, 100, 900), (40, 100, 1)),
+                                         ((513,), (513,)), ((600, 3), (1, 3))])
+def test_prefill_few_rows_over_long_contexts(pa, dt, form, lens, q_lens):
+    """Few query tiles: several CTAs share one tile's KV tiles and merge; some of them see
+    nothing.  Twice the same, captured and replayed too."""
+    b = _prefill_batch(dt, dt, form, 8, 1, 128, 16, 21, lens=lens, q_lens=q_lens)
+    g = b.gpu()
+    out = _prefill(pa, b, g)
+    _close(out, b, form)
+    again = torch.empty_like(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _prefill(pa, b, g, max_query_len=max(q_lens), out=again)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+
+
+@pytest.mark.gpu
+def test_prefill_few_rows_and_a_wait_that_runs_out(pa):
+    """Every CTA of the cluster gives up: zeros, and the next call is whole."""
+    b = _prefill_batch("f16", "f16", "prefix", 8, 1, 128, 16, 22, lens=(1500,), q_lens=(20,))
+    g = b.gpu()
+    try:
+        pa.set_fault_injection(1)
+        pa.set_wait_limit_ns(1_000_000)
+        out = _prefill(pa, b, g)
+        torch.cuda.synchronize()
+        assert pa.get_device_error(clear=True) & pa.DEVERR_TIMEOUT
+        assert not out.any()
+    finally:
+        pa.set_fault_injection(0)
+        pa.set_wait_limit_ns(0)
+    _close(_prefill(pa, b, g), b)
+    assert pa.get_device_error(clear=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_prefill_few_rows_and_unseen_infinities(pa, dt):
+    """The row repair behind a merge: NaN in V of a token that other rows of the tile see."""
+    lens, q_lens = [1200], [16]
+    starts = [1184 if i % 2 else 0 for i in range(16)]
+    b = Batch(dt, dt, lens, q_lens, 8, 2, 128, 16, 33, starts=starts, softcap=20.0)
+    want, tol, _ = b.want()
+    b.kv[1].flatten(0, 1)[b.at(0, 700)] = float("nan")
+    got = _prefill(pa, b).cpu().double()
+    assert ((got - want).abs() <= tol)[1::2].all()
+    assert not torch.isfinite(got[::2]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_prefill_rows_that_see_nothing(pa, dt):
     """Documents that start behind their row, a window of one, an empty chunk: zeros."""
     lens, q_lens = [200, 50, 30], [140, 0, 30]
