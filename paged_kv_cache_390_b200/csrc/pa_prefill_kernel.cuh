@@ -57,7 +57,7 @@
 //   (7.5k clocks a 128-token tile; a 64-token step takes 2.8 to 3.5k).  S and P V are
 //   issued by a warp each: one warp spent as long on its waits as the tensor core on
 //   the products.
-// * The cap is a polynomial on the FMA pipe where the step allows it.  The softmax's own
+// * The cap is a polynomial on the FMA pipe where the row's scores allow it.  The softmax's own
 //   exponential already keeps the special-function unit (4 results a clock and SM
 //   quarter: 2048 clocks per 128 tokens of both query tiles) nearly as busy as the
 //   products keep the tensor core (3584); tanh through ex2 and rcp would triple it.
@@ -177,21 +177,24 @@ enum {
   kBarDrainPv = kBarSFree + 2, kNumBars
 };
 
-// MOD >= 0: y -> factor * tanh(y) for |y| <= 1, as factor * y * Q(y^2): Q of degree 5
-// interpolates tanh(y) / y at the Chebyshev points of y^2 in [0, 1] (4e-7 absolute); with
-// bf16 outputs degree 4 (5e-6; a score at cap 50 is then off by 2.5e-4 at most, where the
-// output's rounding is 2e-3).
-template <typename QT>
+// MOD >= 0: y -> factor * tanh(y) as factor * y * Q(y^2), Q interpolating tanh(y) / y at the
+// Chebyshev points of y^2: of degree 4 for |y| <= 0.625 (1e-7 relative), of degree 6 for
+// |y| <= 1 (4e-8).  Evaluated in 32 bits both are 2e-7 off, relative to the score, so the cap
+// costs no precision however large it is (degree 4 over all of [0, 1], 7e-6, moved weights
+// by 2e-4 at cap 50).  N = 7 holds either: the shorter one's last terms are zero and leave
+// its bits alone.
+constexpr float kCapNear = 0.625f;
+template <int N>
 struct CapPoly {
-  static constexpr int N = std::is_same<QT, __nv_bfloat16>::value ? 5 : 6;
   uint64_t c[N];
-  __device__ __forceinline__ explicit CapPoly(float factor) {
-    constexpr float k4[5] = {0.999992847442627f, -0.332973837852478f, 0.1303347796201706f,
-                             -0.044764984399080276f, 0.009010406211018562f};
-    constexpr float k5[6] = {0.9999994039535522f, -0.3332895040512085f, 0.13280721008777618f,
-                             -0.05158598721027374f, 0.016720855608582497f, -0.0030582291074097157f};
+  __device__ __forceinline__ explicit CapPoly(float factor, bool near = true) {
+    constexpr float kn[7] = {0.9999998807907104f, -0.33331942558288574f, 0.1330437958240509f,
+                             -0.05181591212749481f, 0.015043356455862522f, 0.f, 0.f};
+    constexpr float kw[7] = {0.9999999403953552f, -0.3333282768726349f, 0.13325075805187225f,
+                             -0.053451646119356155f, 0.02027970738708973f, -0.0061943246982991695f,
+                             0.0010380251333117485f};
 #pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = f2splat(factor * (N == 5 ? k4[i % 5] : k5[i]));
+    for (int i = 0; i < N; ++i) c[i] = f2splat(factor * (N == 5 || near ? kn[i] : kw[i]));
   }
   __device__ __forceinline__ uint64_t operator()(uint64_t y, uint64_t add) const {
     const uint64_t z = f2mul(y, y);
@@ -655,20 +658,30 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         }
         auto seen = [&](int c) { return ((bits[c / 32] >> (c % 32)) & 1u) != 0; };
 
-        // The scores.  The cap as a polynomial where every |score| of the warp is within its
-        // unit range (it grows with the score, so the maximum can be taken before it and
-        // the polynomial left to the pass that makes P), else tanh over its whole range; the
-        // bias by packed adds where all of the step is on one side of pos.
+        // The scores.  The cap as a polynomial where every |score| that the row sees is within
+        // its range (it grows with the score, so the maximum can be taken before it and
+        // the polynomial left to the pass that makes P), else tanh over its whole range: each
+        // row's own choice, so that its bits do not depend on what other rows see.  Warps
+        // whose rows all take the short polynomial run it alone.  The bias by packed adds
+        // where all of the step is on one side of pos.
         float factor = a.scale_log2;         // what turns sv into scores in log2 units
-        bool poly = false;
+        bool near = false, own = false;      // this row: the short polynomial; one of the two
+        bool poly = false;                   // the short one in every row of the warp
         if constexpr (CAP) {
           float big[2] = {0.f, 0.f};
+          if (!full) {                       // what the row does not see has no say
+#pragma unroll
+            for (int c = 0; c < NC; ++c) sv[c] = seen(c) ? sv[c] : 0.f;
+          }
 #pragma unroll
           for (int c = 0; c < NC; c += 2)
             big[(c >> 1) & 1] = fmax3_abs(big[(c >> 1) & 1], sv[c], sv[c + 1]);
-          poly = __all_sync(FULL, off || fmaxf(big[0], big[1]) * fabsf(a.cap_in) <= 1.f);
+          const float most = off ? 0.f : fmaxf(big[0], big[1]) * fabsf(a.cap_in);
+          near = most <= kCapNear;
+          own = most <= 1.f;
+          poly = __all_sync(FULL, near);
           factor = a.cap_in;
-          if (!poly) {
+          if (!own) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) sv[c] = a.cap_log2 * tanh_f32(sv[c] * a.cap_in);
             factor = 1.f;
@@ -678,7 +691,6 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
           const int d0 = t_base - row_pos;   // column c is at distance |c + d0|
           const bool before = d0 + NC - 1 <= 0;
           if (__all_sync(FULL, off || before) || __all_sync(FULL, off || d0 >= 0)) {
-            const CapPoly<QT> cap(a.cap_log2);
             const uint64_t f2 = f2splat(factor);
             const float sg = before ? slope : -slope;
             const uint64_t step = f2splat(2.f * sg);
@@ -687,6 +699,7 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
               const float b0 = sg * static_cast<float>(d0 + c32);
               uint64_t b = f2pack(b0, b0 + sg);
               if (CAP && poly) {
+                const CapPoly<5> cap(a.cap_log2);
 #pragma unroll
                 for (int c = c32; c < c32 + 32; c += 2) {
                   const float2 y = f2unpack(cap(f2mul(f2pack(sv[c], sv[c + 1]), f2), b));
@@ -695,9 +708,15 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
                   b = f2add(b, step);
                 }
               } else {
+                const CapPoly<7> cap(a.cap_log2, near);
 #pragma unroll
                 for (int c = c32; c < c32 + 32; c += 2) {
-                  const float2 y = f2unpack(f2fma(f2pack(sv[c], sv[c + 1]), f2, b));
+                  const uint64_t s2 = f2pack(sv[c], sv[c + 1]);
+                  float2 y = f2unpack(f2fma(s2, f2, b));
+                  if constexpr (CAP) {
+                    const float2 yc = f2unpack(cap(f2mul(s2, f2), b));
+                    y = own ? yc : y;
+                  }
                   sv[c] = y.x;
                   sv[c + 1] = y.y;
                   b = f2add(b, step);
@@ -708,16 +727,16 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
             const float d = static_cast<float>(d0);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-              const float y = CAP && poly ? a.cap_log2 * tanh_f32(sv[c] * factor) : sv[c] * factor;
+              const float y = CAP && own ? a.cap_log2 * tanh_f32(sv[c] * factor) : sv[c] * factor;
               sv[c] = fmaf(-slope, fabsf(d + static_cast<float>(c)), y);
             }
           }
-          poly = false;
+          own = poly = false;
           factor = 1.f;
         }
 
         float mx[2] = {-INFINITY, -INFINITY};
-        if (full && factor >= 0.f) {
+        if (full && (CAP ? a.cap_in : a.scale_log2) >= 0.f) {     // so is every row's factor
 #pragma unroll
           for (int c = 0; c < NC; c += 2)
             mx[(c >> 1) & 1] = fmax3(mx[(c >> 1) & 1], sv[c], sv[c + 1]);
@@ -731,7 +750,7 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         float tmax = rmax;
         if (rmax != -INFINITY) {
           tmax = rmax * fabsf(factor);
-          if (CAP && poly) tmax = a.cap_log2 * tanh_f32(tmax);
+          if (CAP && own) tmax = a.cap_log2 * tanh_f32(tmax);
         }
         // the exponent base moves only when the step's maximum exceeds it by more than 8
         const float m_new = tmax > m_run + 8.f ? tmax : m_run;
@@ -746,7 +765,7 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
         auto emit = [&](auto cap_now, auto whole) {
           constexpr bool POLY = decltype(cap_now)::value;    // the cap is still to be taken
           constexpr bool WHOLE = decltype(whole)::value;     // every column is seen
-          const CapPoly<QT> cap(a.cap_log2);
+          const CapPoly<POLY ? 5 : 7> cap(a.cap_log2, near);
           const uint64_t sc2 = f2splat(factor), nb2 = f2splat(-base);
           ps2[0] = ps2[1] = f2splat(0.f);
 #pragma unroll
@@ -756,7 +775,11 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
             for (int e = 0; e < 16; ++e) {
               const int c = 32 * q + 2 * e;
               const uint64_t s2 = f2pack(sv[c], sv[c + 1]);
-              const float2 xx = f2unpack(POLY ? cap(f2mul(s2, sc2), nb2) : f2fma(s2, sc2, nb2));
+              float2 xx = f2unpack(POLY ? cap(f2mul(s2, sc2), nb2) : f2fma(s2, sc2, nb2));
+              if constexpr (CAP && !BIAS && !POLY) {     // rows of the warp differ
+                const float2 xc = f2unpack(cap(f2mul(s2, sc2), nb2));
+                xx = own ? xc : xx;
+              }
               float2 p = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
               if constexpr (!WHOLE) {
                 p.x = seen(c) ? p.x : 0.f;

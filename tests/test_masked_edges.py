@@ -1,0 +1,108 @@
+"""pa_decode_masked and pa_prefill_masked where single bits, infinities and NaN, missing
+blocks or waits that run out decide: against plain 64-bit arithmetic, with tolerances that
+count each rounding."""
+import pytest
+import torch
+
+import _plain64 as p64
+from test_masked import DT, Batch, _decode, _prefill
+
+HEADS = 8
+
+
+def _scores_near(dt, cap, tops, n, seed):
+    """Sequences of n tokens whose scores (before the cap) are known without error and lie
+    within a few units below tops[s] * cap: K holds a score as two numbers of `dt`, q adds
+    them up.  V is zero but for two tokens per (head, dim), whose products with the weights
+    nearly cancel, so that the output shows the weights' ratio and not its own rounding."""
+    g = torch.Generator().manual_seed(seed)
+    t, D = DT[dt], 128
+    b = Batch(dt, dt, [n] * len(tops), [2] * len(tops), HEADS, HEADS, D, 16, seed, softcap=cap)
+    b.scale = 1.0
+    b.q = torch.zeros_like(b.q)
+    b.q[..., :2] = 1.0
+    for s, top in enumerate(tops):
+        x = top * cap - 6.0 * torch.rand((n, HEADS), generator=g, dtype=torch.float64)
+        hi = x.to(t).double()
+        lo = (x - hi).to(t).double()
+        w = torch.softmax(cap * torch.tanh((hi + lo) / cap), dim=0)        # [n, heads]
+        pair = torch.stack([torch.randperm(n - 1, generator=g)[:2] for _ in range(HEADS * D)])
+        pair = pair.view(HEADS, D, 2)
+        k = torch.zeros(n, HEADS, D, dtype=torch.float64)
+        v = torch.zeros(n, HEADS, D, dtype=torch.float64)
+        k[..., 0], k[..., 1] = hi, lo
+        for h in range(HEADS):
+            i, j = pair[h, :, 0], pair[h, :, 1]
+            d = torch.arange(D)
+            v[i, h, d] = 1.0
+            v[j, h, d] = -(w[i, h] / w[j, h])
+        at = [b.at(s, i) for i in range(n)]
+        for x64, val, pool in zip((k, v), b.val, b.kv):
+            pool.flatten(0, 1)[at] = x64.to(t)
+            val.flatten(0, 1)[at] = x64.to(t).double()
+    return b
+
+
+def _ratio_tol(b, want, wv, top, wmax):
+    """Half a step of the output's type; P in two 16-bit parts: 2^-16, and for fp16 2^-25 of
+    the largest weight below its normal range, times the largest V (e^6, two tokens); two
+    weights, whose scores are each off by 6 units of the score in 2^-24 (the tanh to 4, its
+    product with the cap, scale / cap) and 24 of the exponent (16 or less) and the
+    exponential; sums 2^-18."""
+    dx = 2.0 ** -24 * (6 * min(top, 1.0) * b.softcap + 24)
+    floor = 2 * 2.0 ** -25 * 404 * wmax if b.dt == torch.float16 else 0.0
+    tiny = 2.0 ** -25 if b.dt == torch.float16 else 0.0           # fp16's step near 0
+    return (p64.half_step(b.dt) * want.abs() * (1 + 2.0 ** -9)
+            + (2.0 ** -16 + 2 * dx + 2.0 ** -18) * wv + floor + tiny)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("cap", [50.0, 300.0, 3000.0])
+def test_weights_under_any_cap(pa, dt, alibi, cap):
+    """Scores over the whole unit range of the cap and past it (where a row of the same
+    warp needs more than the polynomial): prefill and decode to the 32-bit arithmetic's
+    error, whatever the cap is."""
+    tops = (0.3, 0.6, 0.9, 1.0, 1.3)
+    b = _scores_near(dt, cap, tops, 90, 3)
+    if alibi:                                          # a bias of zero: the biased build
+        b.slopes = torch.zeros(HEADS)
+    pre = _prefill(pa, b).cpu().double()
+    last = [2 * s + 1 for s in range(len(tops))]
+    b1 = Batch.__new__(Batch)
+    b1.__dict__.update(b.__dict__, q=b.q[last].contiguous())
+    dec = _decode(pa, b1).cpu().double()
+    for s, top in enumerate(tops):
+        n = b.lens[s]
+        at = [b.at(s, t) for t in range(n)]
+        k, v = (x.flatten(0, 1)[at] for x in b.val)
+        lo, hi, pos = b.rows[s]
+        o, w, _, wv = p64.attend(b.q[2 * s:2 * s + 2], k, v, 1.0, lo, hi, pos, cap, b.slopes)
+        tol = _ratio_tol(b, o, wv, top, float(w.max()))
+        assert ((pre[2 * s:2 * s + 2] - o).abs() <= tol).all(), \
+            (s, float(((pre[2 * s:2 * s + 2] - o).abs() / tol).max()))
+        assert ((dec[s] - o[1]).abs() <= tol[1]).all(), (s, float(((dec[s] - o[1]).abs() / tol[1]).max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("H,Hkv", [(8, 8), (8, 2)])
+def test_unseen_keys_leave_every_bit_alone(pa, dt, alibi, H, Hkv):
+    """Rows of several documents: the keys of one document small or a hundred times larger
+    (past the polynomial's range); the rows of the others do not see them, and come out
+    the same in every bit."""
+    n = 200
+    starts = [0 if p < 70 else (70 if p < 130 else 130) for p in range(n)]
+    outs = []
+    for mul in (1.0, 100.0):
+        b = Batch(dt, dt, [n, 40], [n, 40], H, Hkv, 128, 16, 12, softcap=8.0, alibi=alibi,
+                  starts=starts + [0] * 40)
+        for t in range(70, 130):
+            b.kv[0].flatten(0, 1)[b.at(0, t)] *= mul
+        for t in range(40, 48):                        # behind the end of sequence 1
+            b.kv[0].flatten(0, 1)[b.at(1, t)] = mul
+        outs.append(_prefill(pa, b).cpu())
+    assert torch.equal(outs[0][:70], outs[1][:70]) and torch.equal(outs[0][130:], outs[1][130:])
+    assert torch.isfinite(outs[1]).all() and not torch.equal(outs[0][70:130], outs[1][70:130])
