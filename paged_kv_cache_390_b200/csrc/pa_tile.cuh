@@ -110,7 +110,9 @@ constexpr bool kFoldV = KIND != kKind16 && std::is_same<QT, __half>::value;
 // The MMA type of the MASK builds: bf16 q over an 8-bit cache goes through the fp16 path
 // too (the codes widen to fp16 in one step, to bf16 in four).  What bf16 has more of is
 // range, so each query head's row is scaled by a power of two to fit (WarpAttn::
-// load_q_wide), and P * s_v by another that follows the largest V scale (vfold).
+// load_q_wide), and its P * s_v by another (WarpAttn::fold) that follows the largest of these
+// products, so that a V scale counts by its token's weight: a far larger scale under a
+// vanishing weight takes nothing from the others.
 template <typename QT, int KIND, bool MASK>
 using mma_type = typename std::conditional<MASK && KIND != kKind16, __half, QT>::type;
 
@@ -119,6 +121,31 @@ using mma_type = typename std::conditional<MASK && KIND != kKind16, __half, QT>:
 __device__ __forceinline__ float pow2_to(float x, int n) {
   const int e = max(-100, min(120, static_cast<int>(__float_as_uint(x) >> 23) - 127));
   return __int_as_float((127 + n - e) << 23);
+}
+
+constexpr float kMostFold = 0x1p110f;   // and the least is 2^-118 (pow2_to)
+
+__device__ __forceinline__ int exponent_of(float pow2) {
+  return static_cast<int>(__float_as_uint(pow2) >> 23) - 127;
+}
+
+// A head's fold (WarpAttn::fold) after its maximum rose by -up to m2: raised by about as
+// much, as all products so far shrank.  Returns what O is multiplied by: 2^up times the
+// fold's change, in (1/2, 2) unless the fold is at its limit.
+__device__ __forceinline__ float follow_max(float& fold, float ref, float m2, float up) {
+  const float n0 = static_cast<float>(exponent_of(fold));
+  const float n = fminf(fmaxf(floorf(m2 - ref), n0), static_cast<float>(exponent_of(kMostFold)));
+  fold = __int_as_float((127 + static_cast<int>(n)) << 23);
+  return fast_exp2(up + (n - n0));
+}
+
+// A head's fold from its products' largest magnitude u > 0 under the maximum m2: u to
+// [4, 8).  Returns what O is multiplied by.
+__device__ __forceinline__ float choose_fold(float& fold, float& ref, float m2, float u) {
+  const float to = pow2_to(u, 2), change = to / fold;
+  ref = m2 - static_cast<float>(exponent_of(to));
+  fold = to;
+  return change;
 }
 
 // Per-lane state of one (sequence, kv head) being accumulated by a warp.
@@ -130,10 +157,12 @@ struct WarpAttn {
   float lsum[2];                    // this lane's share of the running sum
   float lv[2];                      // INT8 under fp16 q: this lane's share of sum P'
   float oacc[T::NMT][4];            // O^T accumulator (d rows, g columns)
-  float vfold;                      // WIDE: the power of two on P * s_v (0: none yet)
+  float fold[2];                    // WIDE: the power of two on P * s_v of heads 2c, 2c + 1
+  float fold_ref[2];                // m2 - log2(fold) when it was chosen
 
   __device__ __forceinline__ void reset() {
-    vfold = 0.f;
+    fold[0] = fold[1] = kMostFold;         // lowered by the first product
+    fold_ref[0] = fold_ref[1] = 0.f;
     m2[0] = m2[1] = -INFINITY;
     lsum[0] = lsum[1] = 0.f;
     lv[0] = lv[1] = 0.f;
@@ -200,7 +229,8 @@ struct WarpAttn {
   __device__ __forceinline__ void finish() {
     if constexpr (kFoldV<QT, KIND>) {
       constexpr uint32_t FULL = 0xffffffffu;
-      const float inv = WIDE ? (vfold > 0.f ? 1.f / vfold : 0.f) : 1.f / T::VFOLD;
+      const float inv = 1.f / (WIDE ? fold[0] : T::VFOLD);
+      const float inv1 = WIDE ? 1.f / fold[1] : inv;
       float b0 = 0.f, b1 = 0.f;
       if constexpr (KIND == kKindI8 && !WIDE) {
         float l0 = lv[0], l1 = lv[1];
@@ -215,9 +245,9 @@ struct WarpAttn {
 #pragma unroll
       for (int mt = 0; mt < T::NMT; ++mt) {
         oacc[mt][0] = fmaf(oacc[mt][0], inv, b0);
-        oacc[mt][1] = fmaf(oacc[mt][1], inv, b1);
+        oacc[mt][1] = fmaf(oacc[mt][1], inv1, b1);
         oacc[mt][2] = fmaf(oacc[mt][2], inv, b0);
-        oacc[mt][3] = fmaf(oacc[mt][3], inv, b1);
+        oacc[mt][3] = fmaf(oacc[mt][3], inv1, b1);
       }
     }
   }
@@ -398,6 +428,7 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   const float ms0 = mn0 == -INFINITY ? 0.f : mn0;
   const float ms1 = mn1 == -INFINITY ? 0.f : mn1;
   const float al0 = fast_exp2(w.m2[0] - ms0), al1 = fast_exp2(w.m2[1] - ms1);
+  const float up0 = w.m2[0] - ms0, up1 = w.m2[1] - ms1;
   w.m2[0] = mn0;
   w.m2[1] = mn1;
   float p0 = fast_exp2(x0 - ms0), p1 = fast_exp2(x1 - ms1);
@@ -409,12 +440,17 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
     w.lv[1] *= al1;
   }
   if (__any_sync(FULL, (al0 != 1.f) || (al1 != 1.f))) {
+    float o0 = al0, o1 = al1;
+    if constexpr (WIDE) {                      // the fold rises as the maximum does
+      o0 = follow_max(w.fold[0], w.fold_ref[0], mn0, up0);
+      o1 = follow_max(w.fold[1], w.fold_ref[1], mn1, up1);
+    }
 #pragma unroll
     for (int mt = 0; mt < T::NMT; ++mt) {
-      w.oacc[mt][0] *= al0;
-      w.oacc[mt][1] *= al1;
-      w.oacc[mt][2] *= al0;
-      w.oacc[mt][3] *= al1;
+      w.oacc[mt][0] *= o0;
+      w.oacc[mt][1] *= o1;
+      w.oacc[mt][2] *= o0;
+      w.oacc[mt][3] *= o1;
     }
   }
 
@@ -422,30 +458,46 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   if constexpr (T::QUANT) {
     // the V scale of each token rides on its P (fp32; poisoned scales of masked
     // tokens never reach a zero P); fp16 q also multiplies by VFOLD
-    float fold = T::VFOLD;
     if constexpr (WIDE) {
-      // the power of two that brings the first V scales to [4, 8), lowered (and O with it)
-      // when a scale would come past 2^10
-      float sm = fmaxf(ok0 ? f.sv0 : 0.f, ok1 ? f.sv1 : 0.f);
+      // times the fold, which brings a head's largest product so far to [2, 2^10]: chosen
+      // anew (and O with it) when one would come past 2^10, the first one too, and raised
+      // with the maximum.  Parts of 2^-25 are then at most 2^-26 of that product.
+      // (One fold per warp by the largest V scale, whatever its token's weight, lost 1.4%
+      // of the other tokens' products to a scale of 2^20.)
+      p0 = p0 != 0.f ? p0 * f.sv0 : 0.f;
+      p1 = p1 != 0.f ? p1 * f.sv0 : 0.f;
+      p2 = p2 != 0.f ? p2 * f.sv1 : 0.f;
+      p3 = p3 != 0.f ? p3 * f.sv1 : 0.f;
+      float u0 = fmaxf(fabsf(p0), fabsf(p2)), u1 = fmaxf(fabsf(p1), fabsf(p3));
+      if (__any_sync(FULL, fmaxf(u0 * w.fold[0], u1 * w.fold[1]) > 1024.f)) {
 #pragma unroll
-      for (int off = 4; off < 32; off <<= 1) sm = fmaxf(sm, __shfl_xor_sync(FULL, sm, off));
-      if (sm > 0.f && (w.vfold == 0.f || sm * w.vfold > 1024.f)) {
-        const float to = pow2_to(sm, 2), down = w.vfold == 0.f ? 1.f : to / w.vfold;
-        w.vfold = to;
+        for (int off = 4; off < 32; off <<= 1) {
+          u0 = fmaxf(u0, __shfl_xor_sync(FULL, u0, off));
+          u1 = fmaxf(u1, __shfl_xor_sync(FULL, u1, off));
+        }
+        float o0 = 1.f, o1 = 1.f;
+        if (u0 * w.fold[0] > 1024.f) o0 = choose_fold(w.fold[0], w.fold_ref[0], ms0, u0);
+        if (u1 * w.fold[1] > 1024.f) o1 = choose_fold(w.fold[1], w.fold_ref[1], ms1, u1);
 #pragma unroll
         for (int mt = 0; mt < T::NMT; ++mt) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w.oacc[mt][k] *= down;
+          w.oacc[mt][0] *= o0;
+          w.oacc[mt][1] *= o1;
+          w.oacc[mt][2] *= o0;
+          w.oacc[mt][3] *= o1;
         }
       }
-      fold = w.vfold;
+      p0 *= w.fold[0];
+      p1 *= w.fold[1];
+      p2 *= w.fold[0];
+      p3 *= w.fold[1];
+    } else {
+      const float v0 = kFoldV<QT, KIND> ? f.sv0 * T::VFOLD : f.sv0;
+      const float v1 = kFoldV<QT, KIND> ? f.sv1 * T::VFOLD : f.sv1;
+      p0 = p0 != 0.f ? p0 * v0 : 0.f;
+      p1 = p1 != 0.f ? p1 * v0 : 0.f;
+      p2 = p2 != 0.f ? p2 * v1 : 0.f;
+      p3 = p3 != 0.f ? p3 * v1 : 0.f;
     }
-    const float v0 = kFoldV<QT, KIND> ? f.sv0 * fold : f.sv0;
-    const float v1 = kFoldV<QT, KIND> ? f.sv1 * fold : f.sv1;
-    p0 = p0 != 0.f ? p0 * v0 : 0.f;
-    p1 = p1 != 0.f ? p1 * v0 : 0.f;
-    p2 = p2 != 0.f ? p2 * v1 : 0.f;
-    p3 = p3 != 0.f ? p3 * v1 : 0.f;
   }
   // P as the B operand.  bf16 keeps 8 significant bits, so P is split into a
   // high and a low bf16 part (two MMAs, ~16 bits); fp16's 11 bits (P in [0, 1])

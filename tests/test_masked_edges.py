@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import _plain64 as p64
-from test_masked import DT, Batch, _decode, _prefill
+from test_masked import DT, Batch, _decode, _prefill, _wide
 
 HEADS = 8
 
@@ -106,3 +106,49 @@ def test_unseen_keys_leave_every_bit_alone(pa, dt, alibi, H, Hkv):
         outs.append(_prefill(pa, b).cpu())
     assert torch.equal(outs[0][:70], outs[1][:70]) and torch.equal(outs[0][130:], outs[1][130:])
     assert torch.isfinite(outs[1]).all() and not torch.equal(outs[0][70:130], outs[1][70:130])
+
+
+def _v_scales(b, how):
+    """Sequence by sequence, a factor on each token's V scale (a power of two), sign included
+    for "signs"."""
+    for s, n in enumerate(b.lens):
+        for t in range(n):
+            f = {"spikes": 2.0 ** 24 if t % 16 == 3 and t < n - 40 else 1.0,
+                 "spikes 2^60": 2.0 ** 60 if t % 16 == 3 and t < n - 100 else 1.0,
+                 "first": 2.0 ** 20 if t < 32 else 1.0,
+                 "falling": 2.0 ** (40 - 40 * t // max(1, n)),
+                 "rising": 2.0 ** (40 * t // max(1, n) - 40),
+                 "signs": -1.0 if t % 3 == 0 else 1.0,
+                 "tiny": 2.0 ** -16}[how]
+            blk, off = divmod(b.at(s, t), b.bs)
+            b.sc[1][blk, :, off] *= f
+            b.val[1][blk, off] *= f
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("cd", ["int8", "fp8"])
+@pytest.mark.parametrize("how", ["spikes", "spikes 2^60", "first", "falling", "rising", "signs", "tiny"])
+@pytest.mark.parametrize("slope", [1.0, 0.125, 0.0])
+def test_decode_bf16_v_scales_by_their_weight(pa, cd, how, slope, wide):
+    """V scales that differ by many powers of two: tokens with the largest ones and a
+    vanishing weight take nothing from the others, as the maximum of the scores rises
+    token by token (a steep bias) or not."""
+    b = Batch("bf16", cd, [300, 40, 150], [1] * 3, 8, 2, 64, 16, 41)
+    b.slopes = slope * torch.linspace(1.0, 1.5, 8)
+    _v_scales(b, how)
+    if wide:
+        _wide(b)
+    got = _decode(pa, b).cpu().double()
+    for s, n in enumerate(b.lens):
+        k, v = (x.flatten(0, 1)[[b.at(s, t) for t in range(n)]] for x in b.val)
+        lo, hi, pos = b.rows[s]
+        o, w, dx, wv = p64.attend(b.q[s:s + 1], k, v, b.scale, lo, hi, pos, 0.0, b.slopes)
+        # P times the V scale in two fp16 parts: 2^-22, and 2^-26 of the largest such product
+        # for each token (times the largest code); weights 2 dx, sums 2^-18
+        top = v.abs().amax(-1).repeat_interleave(4, dim=1).T              # [H, n]
+        peak = (w[0] * top).amax(1)[None, :, None]
+        tol = (p64.half_step(torch.bfloat16) * o.abs() * (1 + 2.0 ** -9)
+               + (2.0 ** -22 + 2 * dx[..., None] + 2.0 ** -18) * wv + n * 2.0 ** -26 * peak)
+        assert torch.isfinite(got[s]).all()
+        assert ((got[s] - o[0]).abs() <= tol[0]).all(), (s, float(((got[s] - o[0]).abs() / tol[0]).max()))
