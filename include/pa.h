@@ -308,7 +308,8 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
  *   Other arguments, types and err_flag as pa_decode_fused.  Short sequences take one
  *   launch (a CTA per sequence and kv head), long or few ones two.  A sequence that sees
  *   nothing gets zeros.  Whatever the rows of unseen tokens hold (infinities, NaN) does not reach
- *   the output or the scores.  A sequence dropped for its length (err_flag) keeps its
+ *   the output or the scores.  Blocks that end before the first seen token are not looked
+ *   up (their entries may be -1).  A sequence dropped for its length (err_flag) keeps its
  *   scores.  Deterministic for a given batch.
  */
 PA_API int pa_decode_masked(void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
@@ -340,7 +341,8 @@ PA_API size_t pa_decode_masked_workspace_bytes(int num_seqs, int num_heads, int 
  *   head_dim 64, fp32, and quantised caches (k_scale, v_scale as pa_decode_v1): these run
  *   on the CUDA cores, one warp per row and head (about 3 TFLOP/s), for completeness.
  *   A row that sees nothing gets zeros.  Unseen rows of K and V do not reach a row's
- *   output, whatever they hold.  A sequence whose lengths or query rows are out of range
+ *   output, whatever they hold; blocks that end before the first token that any row of the
+ *   sequence sees are not looked up.  A sequence whose lengths or query rows are out of range
  *   is skipped, a bad block id read as zeros, as in pa_prefill.
  */
 PA_API int pa_prefill_masked(void* out, const void* q, pa_dtype q_dtype,

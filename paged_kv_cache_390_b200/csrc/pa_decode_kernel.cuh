@@ -37,7 +37,8 @@ __device__ __forceinline__ void write_empty_partial(const DecodeArgs& a, int seq
 // (the 8-bit path is issue- and latency-bound: more resident warps help).
 //
 // MASK (pa_decode_masked): the v1 pass with changed scores, over the tiles from the
-// 16-token boundary at or before the sequence's first seen token.  With running scores
+// 16-token boundary at or before the sequence's first seen token (a block that ends before
+// that token is not looked up: it may be gone).  With running scores
 // asked for, the scores x go to the workspace and, once the CTA has merged its warps and
 // knows every head's log-sum-exp, come back as weights: the CTA holds the whole
 // (sequence, kv head), so no second launch is needed.
@@ -124,8 +125,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     const int t0 = t_begin + 16 * (warp + i * nwarps);
 #pragma unroll
     for (int b = 0; b < T::NBOX; ++b) {
-      const int lb = (t0 + b * T::BOXH) / BS;
-      ids[b] = (i < nmine && lb < nblk_seq) ? __ldg(table + lb) : kBeyond;
+      const int tb = t0 + b * T::BOXH, lb = tb / BS;
+      const bool use = i < nmine && lb < nblk_seq && (!MASK || tb + T::BOXH > lo);
+      ids[b] = use ? __ldg(table + lb) : kBeyond;
     }
   };
 #pragma unroll

@@ -27,7 +27,8 @@
 //
 // MASK (pa_decode_masked): the scores go through a tanh cap and a bias by distance, each
 // sequence's tiles start at the 16-token boundary at or before its first seen token
-// (tokens before it are masked like those past the end), and with running scores asked
+// (tokens before it are masked like those past the end; a block that ends before it is not
+// looked up, as it may be gone), and with running scores asked
 // for, the scores x go to the workspace.  A split unit's records are merged by the next
 // launch (masked_finish_kernel), which finds them from the tile prefix that CTA 0 leaves
 // in place of the counters: one warp merging a unit here took 0.5 us a record, 65 us for
@@ -202,8 +203,9 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
     const int32_t* table = a.block_tables + static_cast<size_t>(lo) * a.max_blocks;
 #pragma unroll
     for (int b = 0; b < T::NBOX; ++b) {
-      const int lb = (t_base + 16 * wn.j + b * T::BOXH) / BS;
-      wn.ids[b] = lb < nblk ? __ldg(table + lb) : kBeyond;
+      const int tb = t_base + 16 * wn.j + b * T::BOXH, lb = tb / BS;
+      const bool use = lb < nblk && (!MASK || tb + T::BOXH > lo_s);   // seen tokens in the box
+      wn.ids[b] = use ? __ldg(table + lb) : kBeyond;
     }
   };
   Win cur, nxt;

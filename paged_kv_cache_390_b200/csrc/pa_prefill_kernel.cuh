@@ -417,12 +417,12 @@ __global__ void __launch_bounds__(prefill_threads<MOD>(), 1)
                       bar(kBarQ), pol);
     }
     // one tile's cache rows, lane b holding box b's (past the cache: the box
-    // is zero-filled)
+    // is zero-filled, as is one that no row of the CTA sees, whose block may be gone)
     auto tile_rows = [&](int j) {
       int row = a.num_blocks * BS;
       if (lane < NBOX) {
         const int t0 = (t_lo + j) * kBN + lane * BOXH;
-        if (t0 < L) {
+        if (t0 < L && (!MASK || (t0 + BOXH > u_lo && t0 < u_hi))) {
           const int blk = __ldg(table + t0 / BS);
           if (blk >= 0 && blk < a.num_blocks) row = blk * BS + t0 % BS;
           else if (a.err_flag) report_error(a.err_flag, kErrBlockId);

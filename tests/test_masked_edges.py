@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import _plain64 as p64
-from test_masked import DT, Batch, _decode, _prefill, _wide
+from test_masked import DT, Batch, _close, _decode, _prefill, _wide
 
 HEADS = 8
 
@@ -152,3 +152,45 @@ def test_decode_bf16_v_scales_by_their_weight(pa, cd, how, slope, wide):
                + (2.0 ** -22 + 2 * dx[..., None] + 2.0 ** -18) * wv + n * 2.0 ** -26 * peak)
         assert torch.isfinite(got[s]).all()
         assert ((got[s] - o[0]).abs() <= tol[0]).all(), (s, float(((got[s] - o[0]).abs() / tol[0]).max()))
+
+
+def _drop_unseen_blocks(b):
+    """-1 in place of every block that ends before the first token that its sequence sees."""
+    for s, (lo, hi, _) in enumerate(b.rows):
+        seen = lo[lo < hi]
+        first = int(seen.min()) if len(seen) else b.lens[s]
+        b.table[s, :first // b.bs] = -1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("flagged", [True, False], ids=["checked", "unchecked"])
+@pytest.mark.parametrize("bs", [8, 16, 32])
+@pytest.mark.parametrize("dt,cd", [("f16", "f16"), ("bf16", "bf16"), ("f32", "f32"), ("f16", "int8"),
+                                   ("bf16", "int8"), ("f16", "fp8"), ("bf16", "fp8")])
+def test_blocks_before_the_window_may_be_gone(pa, dt, cd, bs, flagged):
+    """A window, or a document's start, whose earlier blocks were given back: their entries
+    are not looked up, wherever in a tile the first seen token lies."""
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda") if flagged else None
+    for wide in (False, True):
+        for kw in (dict(window=45), dict(starts=[8 * i + 7 * (i % 3) for i in range(12)])):
+            lens = [60 + 9 * i for i in range(12)]
+            b = Batch(dt, cd, lens, [1] * 12, 8, 2, 128, bs, bs, **kw)
+            if wide:
+                _wide(b)
+            _drop_unseen_blocks(b)
+            sc = torch.zeros((12, 2, max(lens)), device="cuda")
+            per = _close(_decode(pa, b, scores_out=sc, err_flag=flag), b, str(kw))
+            for s, n in enumerate(lens):
+                w, dx = per[s]
+                assert ((sc[s, :, :n].cpu().double() - w).abs() <= p64.scores_tol(w, w, dx)).all()
+    # prefill: few rows (a shared tile), many, and a document that starts inside a block
+    for lens, q_lens in (([700], [9]), ([333, 200], [5, 130]), ([500], [150])):
+        b = Batch(dt, cd, lens, q_lens, 8, 1 if bs == 8 else 2, 128, bs, 7, window=45, softcap=20.0)
+        _drop_unseen_blocks(b)
+        _close(_prefill(pa, b, err_flag=flag), b, str(lens))
+        b = Batch(dt, cd, lens, q_lens, 8, 2, 128, bs, 8, alibi=True,
+                  starts=[n - m - 20 for n, m in zip(lens, q_lens) for _ in range(m)])
+        _drop_unseen_blocks(b)
+        _close(_prefill(pa, b, err_flag=flag), b, str(lens))
+    assert flag is None or int(flag) == 0
+    assert pa.get_device_error(clear=True) == 0
