@@ -327,9 +327,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     for (int w = 0; w < nwarps; ++w) M = fmaxf(M, mred[w * 8 + g]);
     float L = 0.f;
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (M != -INFINITY) {
+    // MASK: a row whose scores are all NaN has no maximum, but is NaN
+    if (MASK || M != -INFINITY) {
+      const float ms = MASK && M == -INFINITY ? 0.f : M;
       for (int w = 0; w < nwarps; ++w) {
-        const float f = fast_exp2(mred[w * 8 + g] - M);
+        const float f = fast_exp2(mred[w * 8 + g] - ms);
         L += lred[w * 8 + g] * f;
         const float* src = ored + (w * 8 + g) * OP + d0;
 #pragma unroll
@@ -382,9 +384,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     if (threadIdx.x < kMaxGroup) {
       float M = -INFINITY, L = 0.f;
       for (int w = 0; w < nwarps; ++w) M = fmaxf(M, mred[w * 8 + threadIdx.x]);
-      if (M != -INFINITY)
-        for (int w = 0; w < nwarps; ++w)
-          L += lred[w * 8 + threadIdx.x] * fast_exp2(mred[w * 8 + threadIdx.x] - M);
+      const float ms = M == -INFINITY ? 0.f : M;
+      for (int w = 0; w < nwarps; ++w)
+        L += lred[w * 8 + threadIdx.x] * fast_exp2(mred[w * 8 + threadIdx.x] - ms);
       lse[threadIdx.x] = threadIdx.x < G ? weight_lse(M, L) : INFINITY;
     }
     __syncthreads();                              // the scores x are this CTA's own writes

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(256)
       if (lg && lane == 0) *lg = x;
       const float mn = fmaxf(m2, x);
       const float al = mn == -INFINITY ? 1.f : exp2f(m2 - mn);
-      const float p = mn == -INFINITY ? 0.f : exp2f(x - mn);
+      const float p = x == -INFINITY ? 0.f : exp2f(x - mn);     // NaN stays NaN, the first too
       l = l * al + p;
 #pragma unroll
       for (int e = 0; e < NE; ++e) acc[e] = fmaf(p, v[e], acc[e] * al);
@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(kFinish, 4)
     for (int t = lane; t < n; t += 32) M = fmaxf(M, record(t)[8 * D + g]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-    if (M != -INFINITY)
-      for (int t = lane; t < n; t += 32)
-        L += record(t)[8 * D + 8 + g] * fast_exp2(record(t)[8 * D + g] - M);
+    const float ms = M == -INFINITY ? 0.f : M;    // then L is 0, or NaN where all scores are
+    for (int t = lane; t < n; t += 32)
+      L += record(t)[8 * D + 8 + g] * fast_exp2(record(t)[8 * D + g] - ms);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
   }

@@ -238,7 +238,7 @@ __device__ __noinline__ void masked_row(const PrefillArgs& a, const int32_t* tab
     x = fmaf(-slope, fabsf(static_cast<float>(pos - t)), x);
     const float mn = fmaxf(m2, x);
     const float al = mn == -INFINITY ? 1.f : fast_exp2(m2 - mn);
-    const float p = mn == -INFINITY ? 0.f : fast_exp2(x - mn);
+    const float p = x == -INFINITY ? 0.f : fast_exp2(x - mn);   // NaN stays NaN, the first too
     l = l * al + p;
 #pragma unroll
     for (int e = 0; e < NE; ++e) acc[e] = fmaf(p, v[e], acc[e] * al);

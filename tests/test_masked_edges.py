@@ -194,3 +194,63 @@ def test_blocks_before_the_window_may_be_gone(pa, dt, cd, bs, flagged):
         _close(_prefill(pa, b, err_flag=flag), b, str(lens))
     assert flag is None or int(flag) == 0
     assert pa.get_device_error(clear=True) == 0
+
+
+NAN = float("nan")
+ALL = [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16"), ("f16", "int8"), ("f16", "fp8"),
+       ("bf16", "int8"), ("bf16", "fp8")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["plain", "cap", "alibi"])
+@pytest.mark.parametrize("dt,cd,D", [(*p, 128) for p in ALL] + [("f16", "f16", 64)])
+def test_prefill_nan_wherever_it_stands(pa, dt, cd, D, form):
+    """A NaN score makes the rows that see it NaN, the first seen token's as well as a later
+    one's, and so does a NaN query; the other rows stay exact."""
+    kw = dict(plain={}, cap=dict(softcap=20.0), alibi=dict(alibi=True))[form]
+    for lens, q_lens, first in (([150], [150], 40), ([700], [12], 600)):
+        n, m = lens[0], q_lens[0]
+        half = n - m // 2                                  # the first rows' document ends here
+        starts = [first if p < half else half for p in range(n - m, n)]
+        for at in (first, first + 3, half - 1):
+            b = Batch(dt, cd, lens, q_lens, 8, 1, D, 16, 5, starts=starts, **kw)
+            want, tol, _ = b.want()
+            blk, off = divmod(b.at(0, at), 16)
+            if cd in DT:
+                b.kv[0][blk, off] = NAN
+            else:
+                b.sc[0][blk, :, off] = NAN
+            b.q[-2, 3] = NAN
+            got = _prefill(pa, b).cpu().double()
+            sees = torch.zeros(m, 8, D, dtype=torch.bool)
+            for r, p in enumerate(range(n - m, n)):
+                sees[r] = starts[r] <= at <= p
+            sees[-2, 3] = True
+            assert torch.isnan(got[sees]).all(), (lens, at)
+            assert ((got - want).abs() <= tol)[~sees].all(), (lens, at)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("dt,cd", ALL)
+def test_decode_nan_wherever_it_stands(pa, dt, cd, softcap, wide):
+    """Decode in both forms: a NaN query, a NaN in the only, the first or a later seen token."""
+    lens = [1, 90, 300, 200, 200]
+    b = Batch(dt, cd, lens, [1] * 5, 8, 2, 128, 16, 9, softcap=softcap, starts=[0, 5, 0, 33, 0])
+    if wide:
+        _wide(b)
+    want, tol, _ = b.want()
+    for s, t in ((0, 0), (1, 5), (2, 150)):
+        blk, off = divmod(b.at(s, t), 16)
+        if cd in DT:
+            b.kv[0][blk, off, 1] = NAN
+        else:
+            b.sc[0][blk, 1, off] = NAN
+    b.q[3, 2] = NAN
+    sees = torch.zeros(want.shape, dtype=torch.bool)
+    sees[:3, 4:] = True                                    # the heads of kv head 1
+    sees[3, 2] = True
+    got = _decode(pa, b).cpu().double()
+    assert torch.isnan(got[sees]).all()
+    assert ((got - want).abs() <= tol)[~sees].all()
