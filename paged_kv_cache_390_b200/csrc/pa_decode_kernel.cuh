@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
       const float before = a.scores_in ? a.scores_in[i] : 0.f;
       float x[8];
       load_scores(a.logits + i * G, t >= lo, G, x);
-      a.scores_out[i] = before + token_weight(x, lse);
+      a.scores_out[i] = before + (t >= lo ? token_weight(x, lse) : 0.f);
     }
   }
 }

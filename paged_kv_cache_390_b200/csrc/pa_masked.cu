@@ -257,7 +257,10 @@ __global__ void __launch_bounds__(kFinish, 4)
   for (int t0 = from; t0 < end; t0 += NT * kFinish) {
     float sum[NT];
 #pragma unroll
-    for (int u = 0; u < NT; ++u) sum[u] = before[u] + token_weight(x[u], lse);
+    for (int u = 0; u < NT; ++u) {
+      const int t = t0 + u * kFinish + threadIdx.x;
+      sum[u] = before[u] + (t >= lo ? token_weight(x[u], lse) : 0.f);
+    }
     if (t0 + NT * kFinish < end) load(t0 + NT * kFinish);
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(256)
   const float before = a.scores_in ? a.scores_in[i] : 0.f;
   float x[kMaxGroup];
   load_scores(a.logits + i * G, t >= sp.lo, G, x);
-  a.scores_out[i] = before + token_weight(x, lse);
+  a.scores_out[i] = before + (t >= sp.lo ? token_weight(x, lse) : 0.f);
 }
 
 template <typename QT, typename KT>

@@ -76,7 +76,8 @@ __device__ __forceinline__ float weight_lse(float M, float L) {
   return L > 0.f || L != L ? M + log2f(L) : INFINITY;
 }
 
-// A token's weight, summed over the heads (lse: 8 of them, +inf past G).
+// A seen token's weight, summed over the heads (lse: 8 of them, +inf past G).  Not for
+// others: where a head's row is NaN, -inf would give NaN too.
 __device__ __forceinline__ float token_weight(const float (&x)[8], const float* lse) {
   float w = 0.f;
 #pragma unroll

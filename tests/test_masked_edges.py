@@ -254,3 +254,34 @@ def test_decode_nan_wherever_it_stands(pa, dt, cd, softcap, wide):
     got = _decode(pa, b).cpu().double()
     assert torch.isnan(got[sees]).all()
     assert ((got - want).abs() <= tol)[~sees].all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("dt,cd", [("f32", "f32"), ("f16", "f16"), ("bf16", "int8")])
+def test_running_scores_of_rows_that_are_nan(pa, dt, cd, wide):
+    """Tokens that the row does not see keep their scores though its weights are NaN, and
+    so do the scores of the other kv head."""
+    lens, starts = [200, 90], [77, 40]
+    b = Batch(dt, cd, lens, [1, 1], 8, 2, 128, 16, 9, starts=starts)
+    if wide:
+        _wide(b)
+    _, _, per = b.want()
+    for s, t in ((0, 77), (1, 80)):
+        blk, off = divmod(b.at(s, t), 16)
+        if cd in DT:
+            b.kv[0][blk, off, 1] = NAN
+        else:
+            b.sc[0][blk, 1, off] = NAN
+    before = torch.rand((2, 2, 210), generator=torch.Generator().manual_seed(1))
+    sc = before.cuda()
+    _decode(pa, b, scores_in=sc, scores_out=sc)
+    sc = sc.cpu()
+    for s, n in enumerate(lens):
+        lo = starts[s]
+        assert torch.equal(sc[s, :, :lo], before[s, :, :lo])
+        assert torch.equal(sc[s, :, n:], before[s, :, n:])
+        assert torch.isnan(sc[s, 1, lo:n]).all()
+        w, dx = per[s]
+        total = before[s, 0, :n].double() + w[0]
+        assert ((sc[s, 0, :n].double() - total).abs() <= p64.scores_tol(total, w[0], dx[0])).all()
