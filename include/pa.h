@@ -310,7 +310,8 @@ PA_API int pa_copy_blocks(const void* src_k_cache, const void* src_v_cache,
  *   nothing gets zeros.  Whatever the rows of unseen tokens hold (infinities, NaN) does not reach
  *   the output or the scores.  Blocks that end before the first seen token are not looked
  *   up (their entries may be -1).  A sequence dropped for its length (err_flag) keeps its
- *   scores.  Deterministic for a given batch.
+ *   scores; so does a (sequence, kv head) whose tiles did not arrive in time
+ *   (PA_DEVERR_TIMEOUT), which gets zeros.  Deterministic for a given batch.
  */
 PA_API int pa_decode_masked(void* out, const void* q, pa_dtype q_dtype, const void* k_cache,
                             const void* v_cache, pa_dtype cache_dtype, const float* k_scale,
@@ -622,7 +623,8 @@ PA_API int pa_set_wait_limit_ns(unsigned long long limit_ns);
  * in every decode warp the first pipeline stage is never armed, so the wait
  * on it can only end by running out its time limit (set one with
  * pa_set_wait_limit_ns first).  The kernel then reports PA_DEVERR_TIMEOUT and
- * returns normally; no GPU fault is involved.  Applies to later calls.
+ * returns normally; no GPU fault is involved.  Mode 3, in pa_decode_masked alone: the
+ * stage of each warp's last tile, where the warp has more than two.  Applies to later calls.
  */
 PA_API int pa_set_fault_injection(int mode);
 

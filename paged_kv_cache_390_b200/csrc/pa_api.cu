@@ -196,7 +196,7 @@ PA_API int pa_set_prefetch_tiles(int tiles_per_warp) {
 }
 
 PA_API int pa_set_fault_injection(int mode) {
-  if (mode < 0 || mode > 1) return PA_ERR_INVALID_ARG;
+  if (mode != 0 && mode != 1 && mode != 3) return PA_ERR_INVALID_ARG;
   g_inject.store(mode, std::memory_order_relaxed);
   return PA_OK;
 }

@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
 
   const uint64_t pol = policy_evict_first();
 
+  const int never = a.inject == 1 ? 0 : MASK && a.inject == 3 && nmine > 2 ? nmine - 1 : -1;
+
   // Issue the loads of this warp's i-th tile into stage s (whole warp calls).
   auto issue = [&](int i, int s) {
     const int wdx = i >> 5;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     int blk[T::NBOX];
 #pragma unroll
     for (int b = 0; b < T::NBOX; ++b) blk[b] = __shfl_sync(FULL, ids_cur[b], i & 31);
-    if (a.inject == 1 && i == 0) return;          // test hook: this stage never arrives
+    if (i == never) return;                       // test hook: this stage never arrives
     armed |= 1u << s;
     if (lane == 0) {
       const uint32_t st = wbase + static_cast<uint32_t>(s * T::STAGE);
@@ -296,7 +298,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     wa.lsum[0] += __shfl_xor_sync(FULL, wa.lsum[0], off);
     wa.lsum[1] += __shfl_xor_sync(FULL, wa.lsum[1], off);
   }
-  __syncthreads();   // every warp is done with its stages
+  // every warp is done with its stages; MASK: a warp lost tiles, and with them the unit
+  bool lost = false;
+  if constexpr (MASK) lost = __syncthreads_or(dead) != 0;
+  else __syncthreads();
   constexpr int OP = D + 4;
   float* ored = reinterpret_cast<float*>(smem_raw + (sbase - sraw));
   float* mred = ored + nwarps * 8 * OP;
@@ -358,7 +363,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
         M = M2;
       }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L > 0.f && !lost ? 1.f / L : 0.f;
+    if (MASK && lost) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0.f;
+    }
     if (v1) {
       uint4 pk;
       pk.x = pack2<QT>(o[0] * inv, o[1] * inv);
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     }
   }
   if constexpr (MASK) {
-    if (!a.scores_out || bad) return;             // a skipped sequence keeps its scores
+    if (!a.scores_out || bad || lost) return;     // a skipped or lost unit keeps its scores
     __shared__ float lse[kMaxGroup];
     if (threadIdx.x < kMaxGroup) {
       float M = -INFINITY, L = 0.f;

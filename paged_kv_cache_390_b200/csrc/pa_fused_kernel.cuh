@@ -32,7 +32,8 @@
 // for, the scores x go to the workspace.  A split unit's records are merged by the next
 // launch (masked_finish_kernel), which finds them from the tile prefix that CTA 0 leaves
 // in place of the counters: one warp merging a unit here took 0.5 us a record, 65 us for
-// 2 sequences of 1000 tokens.
+// 2 sequences of 1000 tokens.  A warp whose wait runs out marks its units as lost from the
+// open one on; they come out as zeros, and the next launch leaves their scores alone.
 #pragma once
 
 #include <atomic>
@@ -48,6 +49,10 @@ namespace pa {
 __device__ __forceinline__ void discard_l2_line(const void* p) {
   asm volatile("discard.global.L2 [%0], 128;" ::"l"(p) : "memory");
 }
+
+// MASK: the place in a partial record that tells whether its warp lost tiles.
+template <int D>
+constexpr int kLostAt = 8 * D + 16;
 
 __device__ __forceinline__ void put_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put_elem(__half* p, float v) { *p = __float2half_rn(v); }
@@ -165,6 +170,15 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
   const int t_lo = idle ? 0 : static_cast<int>(range_start(wme));
   const int nmine = idle ? 0 : static_cast<int>(range_start(wme + 1) - t_lo);
 
+  auto seq_of = [&](int g) {                      // the sequence of tile g
+    int lo = 0, hi = NS;                          // C[lo] <= g < C[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (C[mid] <= g) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
   // Window: lane l describes tile (32 * window + l) of this warp's range.
   struct Win {
     int ids[T::NBOX];
@@ -179,12 +193,7 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
     for (int b = 0; b < T::NBOX; ++b) wn.ids[b] = kBeyond;
     if (i >= nmine) return;
     const int g = t_lo + i;
-    int lo = 0, hi = NS;                          // C[lo] <= g < C[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (C[mid] <= g) lo = mid;
-      else hi = mid;
-    }
+    const int lo = seq_of(g);
     const int nt = (C[lo + 1] - C[lo]) / Hkv;
     const int off = g - C[lo];
     wn.seq = lo;
@@ -240,6 +249,7 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
   uint32_t armed = 0;
   const uint64_t pol = policy_evict_first();
 
+  const int never = a.inject == 1 ? 0 : MASK && a.inject == 3 && nmine > 2 ? nmine - 1 : -1;
   auto issue = [&](int i, int s) {
     const int wdx = i >> 5;
     if (wdx != win_cur) {
@@ -259,7 +269,7 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
       len = __shfl_sync(FULL, cur.len, src);
       lo = __shfl_sync(FULL, cur.lo, src);
     }
-    if (a.inject == 1 && i == 0) return;          // test hook: this stage never arrives
+    if (i == never) return;                       // test hook: this stage never arrives
     armed |= 1u << s;
     if (lane == 0) {
       const uint32_t st = wbase + static_cast<uint32_t>(s * STG);
@@ -367,7 +377,10 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
       rec[8 * D + 8 + 2 * c] = l0;
       rec[8 * D + 8 + 2 * c + 1] = l1;
     }
-    if constexpr (MASK) return;
+    if constexpr (MASK) {
+      if (lane == 0) rec[kLostAt<D>] = 0.f;
+      return;
+    }
     __threadfence();
     __syncwarp();
     int prev = 0;
@@ -513,7 +526,7 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
 
   int si = 0;
   uint32_t ph = 0;
-  bool dead = false;
+  bool dead = false, opened = false;
   int cur_seq = 0, cur_kvh = 0, seg_j0 = 0, prev_j = 0;
   bool first_seg = true;
   ScoreMod mod;
@@ -554,6 +567,7 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
       cur_seq = seq;
       cur_kvh = kvh;
       seg_j0 = j;
+      opened = true;
       if constexpr (MASK) {
         if (a.slopes) {
           if (2 * c < G) mod.slope[0] = a.slopes[kvh * G + 2 * c] * kLog2e;
@@ -584,6 +598,25 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
   }
   if (dead) {
     if (lane == 0) report_error(a.err_flag, kErrTimeout);
+    if constexpr (MASK) {
+      int g = t_lo;                                // the open segment's first tile, then the others'
+      if (opened) g = C[cur_seq] + cur_kvh * ((C[cur_seq + 1] - C[cur_seq]) / Hkv) + seg_j0;
+      const int g_end = t_lo + nmine;
+      while (g < g_end) {
+        const int seq = seq_of(g), nt = (C[seq + 1] - C[seq]) / Hkv;
+        const int kvh = (g - C[seq]) / nt, start = C[seq] + kvh * nt, end = min(g_end, start + nt);
+        if (g == start && end == start + nt) {     // a whole unit
+          const size_t prow = static_cast<size_t>(seq) * a.num_heads + static_cast<size_t>(kvh) * G;
+          QT* o = reinterpret_cast<QT*>(a.out) + prow * D;
+          for (int e = 8 * lane; e < G * D; e += 256)
+            *reinterpret_cast<uint4*>(o + e) = make_uint4(0u, 0u, 0u, 0u);
+          if (a.lse && lane < G) a.lse[prow + lane] = -INFINITY;   // no row's own: lost
+        } else if (lane == 0) {
+          a.partials[static_cast<size_t>(2 * wme + (g == t_lo ? 0 : 1)) * REC + kLostAt<D>] = 1.f;
+        }
+        g = end;
+      }
+    }
   } else if (nmine > 0) {
     finalize(cur_seq, cur_kvh, seg_j0, prev_j, first_seg);
   }

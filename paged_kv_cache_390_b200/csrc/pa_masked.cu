@@ -201,8 +201,12 @@ __global__ void __launch_bounds__(kFinish, 4)
     if (bad || from >= have) return;              // a skipped sequence keeps its scores
     load(from);
   }
+  // a unit that lost tiles to a wait that ran out: a marked record, or its own mark
+  bool lost = n == 1 && a.lse && g < G && a.lse[row] == -INFINITY;
   float M = -INFINITY, L = 0.f;
   if (n > 1 && g < G) {
+    for (int t = lane; t < n; t += 32) lost = lost || record(t)[kLostAt<D>] != 0.f;
+    lost = __any_sync(FULL, lost);
     for (int t = lane; t < n; t += 32) M = fmaxf(M, record(t)[8 * D + g]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
@@ -242,7 +246,11 @@ __global__ void __launch_bounds__(kFinish, 4)
       acc.z += __shfl_xor_sync(FULL, acc.z, 16);
       acc.w += __shfl_xor_sync(FULL, acc.w, 16);
     }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // NaN stays NaN
+    float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);        // NaN stays NaN
+    if (lost) {
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      inv = 0.f;
+    }
     if (sub == 0) {
       uint2 pk;
       pk.x = pack2<QT>(acc.x * inv, acc.y * inv);
@@ -252,7 +260,7 @@ __global__ void __launch_bounds__(kFinish, 4)
     return;
   }
   if (lane == 0) lse[g] = g >= G ? INFINITY : (n == 1 ? a.lse[row] : weight_lse(M, L));
-  __syncthreads();
+  if (__syncthreads_or(lost)) return;             // its scores stay
   const int end = min(have, from + kTokens);
   for (int t0 = from; t0 < end; t0 += NT * kFinish) {
     float sum[NT];

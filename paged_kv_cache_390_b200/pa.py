@@ -741,5 +741,6 @@ def set_pdl(mode: int = 1) -> None:
 
 def set_fault_injection(mode: int = 0) -> None:
     """Test hook: mode 1 withholds each decode warp's first stage so its bounded
-    wait runs out (reported as DEVERR_TIMEOUT); 0 turns it off."""
+    wait runs out (reported as DEVERR_TIMEOUT), mode 3 each masked decode warp's last
+    one, where it has more than two; 0 turns it off."""
     _check(lib().pa_set_fault_injection(int(mode)), "pa_set_fault_injection")

@@ -285,3 +285,80 @@ def test_running_scores_of_rows_that_are_nan(pa, dt, cd, wide):
         w, dx = per[s]
         total = before[s, 0, :n].double() + w[0]
         assert ((sc[s, 0, :n].double() - total).abs() <= p64.scores_tol(total, w[0], dx[0])).all()
+
+
+WAIT_LENS = [90, 200, 700, 16, 40, 333, 1, 512]
+
+
+def _wait_batch(pa, dt, cd, wide):
+    b = Batch(dt, cd, WAIT_LENS, [1] * len(WAIT_LENS), 8, 2, 128, 16, 19, softcap=20.0)
+    if wide:
+        _wide(b)
+    g = b.gpu()
+    ws = pa.MaskedWorkspace(len(WAIT_LENS), 8, 2, 128, 700)
+    ws.buf.fill_(0x7E)                                     # 8e37 wherever a float is read
+    before = torch.rand((len(WAIT_LENS), 2, 700), generator=torch.Generator().manual_seed(1))
+    return b, g, ws, before
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("dt,cd", [("bf16", "bf16"), ("f16", "int8"), ("bf16", "fp8")])
+def test_decode_tiles_that_never_arrive(pa, dt, cd, wide):
+    """Zeros, and the running scores as they were, whatever the workspace held."""
+    b, g, ws, before = _wait_batch(pa, dt, cd, wide)
+    sc = before.cuda()
+    try:
+        pa.set_fault_injection(1)
+        pa.set_wait_limit_ns(1_000_000)
+        out = _decode(pa, b, g, scores_in=sc, scores_out=sc, workspace=ws)
+        torch.cuda.synchronize()
+        assert pa.get_device_error(clear=True) & pa.DEVERR_TIMEOUT
+    finally:
+        pa.set_fault_injection(0)
+        pa.set_wait_limit_ns(0)
+    assert not out.any() and torch.equal(sc.cpu(), before)
+    _close(_decode(pa, b, g, scores_in=sc, scores_out=sc, workspace=ws), b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("dt,cd", [("bf16", "bf16"), ("f16", "int8"), ("bf16", "fp8")])
+@pytest.mark.parametrize("mode,limit", [(3, 1_000_000), (0, 1)], ids=["last tiles", "no wait"])
+def test_decode_some_tiles_that_never_arrive(pa, dt, cd, wide, mode, limit):
+    """Each (sequence, kv head) is right, scores and all, or is zeros with its scores as they
+    were."""
+    b, g, ws, before = _wait_batch(pa, dt, cd, wide)
+    want, tol, per = b.want()
+    results = []
+    try:
+        pa.set_fault_injection(mode)
+        pa.set_wait_limit_ns(limit)
+        for scored in (True, False):
+            ws.buf.fill_(0x7E)
+            sc = before.cuda() if scored else None
+            out = _decode(pa, b, g, scores_in=sc, scores_out=sc, workspace=ws)
+            torch.cuda.synchronize()
+            results.append((out.cpu().double(), sc.cpu() if scored else None,
+                            bool(pa.get_device_error(clear=True) & pa.DEVERR_TIMEOUT)))
+    finally:
+        pa.set_fault_injection(0)
+        pa.set_wait_limit_ns(0)
+    for out, sc, flag in results:
+        lost = 0
+        for i, n in enumerate(b.lens):
+            for k in range(2):
+                x = slice(4 * k, 4 * k + 4)
+                if not out[i, x].any():
+                    lost += 1
+                    assert sc is None or torch.equal(sc[i, k], before[i, k])
+                    continue
+                assert ((out[i, x] - want[i, x]).abs() <= tol[i, x]).all(), (i, k)
+                if sc is not None:
+                    w, dx = per[i]
+                    total = before[i, k, :n].double() + w[k]
+                    assert ((sc[i, k, :n].double() - total).abs()
+                            <= p64.scores_tol(total, w[k], dx[k])).all(), (i, k)
+                    assert torch.equal(sc[i, k, n:], before[i, k, n:])
+        assert flag == (lost > 0)
+        assert mode == 0 or 0 < lost < 2 * len(b.lens), lost
