@@ -147,12 +147,15 @@ __global__ void __launch_bounds__(256)
 // loads one after another, so a CTA has many tokens and four fit an SM (1024 tokens, two
 // per SM: 37 us for 8 x 32k tokens).
 // One warp per query head of the kv head; a merge keeps 8 records' loads in flight.
+// The prefix and the records are the preceding launch's writes, which this one may overlap:
+// their pointers carry no __restrict__, which would let the compiler take them for constant
+// and load them on the read-only path or before griddepcontrol.wait.
 constexpr int kFinish = 256, kTokens = 4096;
 
 template <typename QT, int D>
 __global__ void __launch_bounds__(kFinish, 4)
-    masked_finish_kernel(const __grid_constant__ MaskedArgs a, const int* __restrict__ prefix,
-                         const float* __restrict__ records, int warps) {
+    masked_finish_kernel(const __grid_constant__ MaskedArgs a, const int* prefix,
+                         const float* records, int warps) {
   constexpr uint32_t FULL = 0xffffffffu;
   constexpr int REC = 8 * D + 32;
   __shared__ float lse[kMaxGroup];
