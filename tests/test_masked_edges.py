@@ -362,3 +362,78 @@ def test_decode_some_tiles_that_never_arrive(pa, dt, cd, wide, mode, limit):
                     assert torch.equal(sc[i, k, n:], before[i, k, n:])
         assert flag == (lost > 0)
         assert mode == 0 or 0 < lost < 2 * len(b.lens), lost
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cta", "persistent"])
+@pytest.mark.parametrize("cd", ["int8", "fp8"])
+@pytest.mark.parametrize("vs", [1.0, 2.0 ** -6, 2.0 ** -9, 2.0 ** 8])
+@pytest.mark.parametrize("slope", [0.0, 0.125])
+def test_decode_f16_v_scales_of_any_size(pa, cd, vs, slope, wide):
+    """fp16 queries over 8-bit caches: values of a few hundredths or thousandths, or of
+    hundreds, to the output's rounding."""
+    lens = [300, 40, 900]
+    b = Batch("f16", cd, lens, [1] * 3, 8, 2, 64, 16, 43, qmul=0.5)
+    b.slopes = slope * torch.linspace(1.0, 1.5, 8)
+    b.sc[1] *= vs
+    b.val[1] = b.val[1] * vs
+    if wide:
+        _wide(b)
+    got = _decode(pa, b).cpu().double()
+    for s, n in enumerate(lens):
+        k, v = (x.flatten(0, 1)[[b.at(s, t) for t in range(n)]] for x in b.val)
+        lo, hi, pos = b.rows[s]
+        o, w, dx, wv = p64.attend(b.q[s:s + 1], k, v, b.scale, lo, hi, pos, 0.0, b.slopes)
+        # as above, and half of fp16's step near 0
+        peak = (w[0] * v.abs().amax(-1).repeat_interleave(4, dim=1).T).amax(1)[None, :, None]
+        tol = (p64.half_step(torch.float16) * o.abs() * (1 + 2.0 ** -9) + 2.0 ** -25
+               + (2.0 ** -22 + 2 * dx[..., None] + 2.0 ** -18) * wv + n * 2.0 ** -26 * peak)
+        assert ((got[s] - o[0]).abs() <= tol[0]).all(), (s, float(((got[s] - o[0]).abs() / tol[0]).max()))
+
+
+def _parts_batch(cd, prefill):
+    if prefill:
+        return Batch("f16", cd, [300, 90, 520], [40, 90, 130], 8, 2, 128, 16, 51, softcap=30.0)
+    return Batch("f16", cd, [100, 333, 640, 700], [1] * 4, 32, 4, 128, 16, 52, softcap=30.0)
+
+
+def _off(out, want):
+    return float((out - want).norm() / want.norm())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form,cd", [(f, c) for f in ("one-cta", "persistent")
+                                     for c in ("f16", "int8", "fp8")] + [("prefill", "f16")])
+def test_fp16_weights_go_in_as_two_parts(pa, form, cd):
+    """The result is off by little more than its own rounding: the weights' two fp16 parts are
+    2^-22 (one alone is as far off as the output, see below), 32-bit arithmetic and INT8's
+    bias a few 2^-18, against a rounding of about 2^-12 in the mean."""
+    b = _parts_batch(cd, form == "prefill")
+    if form == "persistent":
+        _wide(b)
+    want, _, _ = b.want()
+    got = (_prefill if form == "prefill" else _decode)(pa, b).cpu().double()
+    assert _off(got, want) <= 1.05 * _off(want.half().double(), want) + 5e-6
+
+
+@pytest.mark.parametrize("prefill", [False, True])
+def test_that_bound_tells_one_part_from_two(prefill):
+    b = _parts_batch("f16", prefill)
+    want, _, _ = b.want()
+    one, two, r = [], [], 0
+    for s, (n, m) in enumerate(zip(b.lens, b.q_lens)):
+        k, v = (x.flatten(0, 1)[[b.at(s, t) for t in range(n)]] for x in b.val)
+        lo, hi, pos = b.rows[s]
+        _, w, _, _ = p64.attend(b.q[r:r + m], k, v, b.scale, lo, hi, pos, b.softcap)
+        p = w / w.amax(-1, keepdim=True)                   # as the kernels hold it
+        vv = v.repeat_interleave(b.H // b.Hkv, dim=1)
+        h = p.half().double()
+        for parts, to in ((h, one), (h + (p - h).half().double(), two)):
+            to.append(torch.einsum("rhn,nhd->rhd", parts, vv) / p.sum(-1, keepdim=True))
+        r += m
+    bound = 1.05 * _off(want.half().double(), want) + 5e-6
+    assert _off(torch.cat(two).half().double(), want) <= bound
+    # one part: each weight off by up to 2^-12 of its binade, as the output is once more; over
+    # many weights that adds 2^-11 / sqrt(12) / 1.4 = 1.0e-4 to the rounding's 2.0e-4, as
+    # sqrt(2.0^2 + 1.0^2) = 2.24, which is past 1.05 * 2.0
+    assert _off(torch.cat(one).half().double(), want) > bound
