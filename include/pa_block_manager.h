@@ -104,9 +104,12 @@ PA_API int pa_bm_swap_in(pa_block_manager* m, const int64_t* seq_ids, int num_se
  * blocks, written to new_tables int32 [num_seqs][max_blocks] (padding -1), and lets go of
  * its old ones.  Take the old tables with pa_bm_build_batch before this call, and enqueue
  * pa_evict before anything that writes blocks handed out later.  All fresh blocks are
- * taken before any old one is released, so no new block is a source of the same call.
- * Each kv head of such a sequence keeps its own tokens: from here on its blocks are not
- * offered to the prefix cache. */
+ * taken before any old one is released, so no new block is a source of the same call:
+ * with fewer free, PA_ERR_NO_SPACE and nothing changed (keep a reserve of one cut sequence's
+ * blocks and evict sequence by sequence where the pool is nearly full).
+ * Each kv head of a sequence that is cut keeps its own tokens: from here on its blocks are
+ * not offered to the prefix cache.  A sequence of at most num_keep tokens is moved whole and
+ * goes on filling the prefix cache as before. */
 PA_API int pa_bm_evict(pa_block_manager* m, const int64_t* seq_ids, int num_seqs, int num_keep,
                        int32_t* new_tables, int max_blocks);
 

@@ -140,7 +140,8 @@ class BlockManager:
 
     def evict(self, seq_ids, num_keep: int):
         """New block tables int32 [n, max_blocks] (padded with -1) for sequences cut to
-        num_keep tokens by ``pa.evict``; take their old ones (``build_batch``) first."""
+        num_keep tokens by ``pa.evict``; take their old ones (``build_batch``) first.  All the
+        new blocks have to be free before the call (else PA_ERR_NO_SPACE, nothing changed)."""
         ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
         width = -(-num_keep // self.block_size) if num_keep > 0 else 1
         tables = np.empty((len(ids), width), dtype=np.int32)

@@ -369,8 +369,10 @@ PA_API int pa_bm_evict(pa_block_manager* m, const int64_t* seq_ids, int num_seqs
     const size_t n = blocks_of(s);
     for (size_t b = 0; b < n; ++b) fresh[i].push_back(m->take_gpu());
     s.blocks.swap(fresh[i]);                     // fresh[i] now holds the old ones
-    s.tokens.resize(std::min<size_t>(s.tokens.size(), num_keep));
-    s.cut = true;
+    if (s.tokens.size() > static_cast<size_t>(num_keep)) {   // else copied whole, in its order
+      s.tokens.resize(num_keep);
+      s.cut = true;
+    }
     int32_t* row = new_tables + static_cast<size_t>(i) * max_blocks;
     std::copy(s.blocks.begin(), s.blocks.end(), row);
     std::fill(row + n, row + max_blocks, -1);
