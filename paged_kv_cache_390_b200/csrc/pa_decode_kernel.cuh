@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, KIND == kKind16 ? 0 : 2)
     if (lane == 0) report_error(a.err_flag, kErrTimeout);
     wa.reset();
   } else {
-    wa.template finish<WIDE>();
+    wa.template finish<MASK, WIDE>();
   }
 
   // ---- merge the warps of the CTA through shared memory

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kFusedWarps * 32, MINB)
   // Close the current segment (tiles j0..j1 of unit (seq, kvh)).
   auto finalize = [&](int seq, int kvh, int j0, int j1, bool first) {
     const int nt = (C[seq + 1] - C[seq]) / Hkv;
-    wa.template finish<WIDE>();
+    wa.template finish<MASK, WIDE>();
     float l0 = wa.lsum[0], l1 = wa.lsum[1];
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {

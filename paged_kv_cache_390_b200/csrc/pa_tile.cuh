@@ -224,15 +224,16 @@ struct WarpAttn {
 
   // End of a unit's tiles (before its lanes' results are combined): fp16 q over an
   // 8-bit cache accumulated sum P' (bias + code) with P' = P * s_v * VFOLD; take
-  // the bias term out (INT8 codes enter as 1152 + c) and the fold factor.
-  template <bool WIDE = false>
+  // the bias term out (INT8 codes enter as 1152 + c, but exact in the MASK builds) and the
+  // fold factor.
+  template <bool MASK = false, bool WIDE = false>
   __device__ __forceinline__ void finish() {
     if constexpr (kFoldV<QT, KIND>) {
       constexpr uint32_t FULL = 0xffffffffu;
       const float inv = 1.f / (WIDE ? fold[0] : T::VFOLD);
       const float inv1 = WIDE ? 1.f / fold[1] : inv;
       float b0 = 0.f, b1 = 0.f;
-      if constexpr (KIND == kKindI8 && !WIDE) {
+      if constexpr (KIND == kKindI8 && !MASK) {
         float l0 = lv[0], l1 = lv[1];
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
@@ -435,7 +436,7 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   float p2 = fast_exp2(x2 - ms0), p3 = fast_exp2(x3 - ms1);
   w.lsum[0] = w.lsum[0] * al0 + (p0 + p2);
   w.lsum[1] = w.lsum[1] * al1 + (p1 + p3);
-  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8 && !WIDE) {
+  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8 && !MASK) {
     w.lv[0] *= al0;
     w.lv[1] *= al1;
   }
@@ -511,15 +512,10 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
   const uint32_t l23 = pack2<QT>(p2 - f23.x, p3 - f23.y);
   const uint32_t bh0 = movmatrix_trans(h01), bh1 = movmatrix_trans(h23);
   const uint32_t bl0 = movmatrix_trans(l01), bl1 = movmatrix_trans(l23);
-  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8 && !WIDE) {
+  if constexpr (kFoldV<QT, KIND> && KIND == kKindI8 && !MASK) {
     // the sum of the P' the MMAs see (fp16-rounded), for the bias of the codes
     w.lv[0] += f01.x + f23.x;
     w.lv[1] += f01.y + f23.y;
-    if constexpr (kSplitP) {
-      const float2 e01 = unpack2<QT>(l01), e23 = unpack2<QT>(l23);
-      w.lv[0] += e01.x + e23.x;
-      w.lv[1] += e01.y + e23.y;
-    }
   }
 
   uint32_t mk01 = ~0u, mk23 = ~0u;
@@ -550,9 +546,10 @@ __device__ __forceinline__ void tile_compute(WarpAttn<QT, KIND, D, BS>& w,
       for (int hh = 0; hh < 2; ++hh) {
         const int mt = 2 * q + hh;
         uint32_t af[4];
-        if constexpr (WIDE && KIND == kKindI8) {
-          // the same pairs as exact codes: the bias's own rounding (2e-5 of a V scale)
-          // would show in a bf16 output near 0
+        if constexpr (MASK && KIND == kKindI8) {
+          // the same pairs as exact codes: under the bias O holds 1152 times the weights' sum,
+          // whose roundings stay when the bias is taken out (30k tokens: 1.7e-3 of an fp16
+          // output, where its own rounding is 2e-4)
           const uint32_t x0 = f.vf[q][2 * hh] ^ 0x80808080u;
           const uint32_t x1 = f.vf[q][2 * hh + 1] ^ 0x80808080u;
           af[0] = int8x2_biased_to_f16x2<0x5240u>(x0);

@@ -437,3 +437,18 @@ def test_that_bound_tells_one_part_from_two(prefill):
     # many weights that adds 2^-11 / sqrt(12) / 1.4 = 1.0e-4 to the rounding's 2.0e-4, as
     # sqrt(2.0^2 + 1.0^2) = 2.24, which is past 1.05 * 2.0
     assert _off(torch.cat(one).half().double(), want) > bound
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt,cd", [("f16", "int8"), ("f16", "fp8"), ("f16", "f16"), ("bf16", "int8")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_long_contexts_to_the_rounding(pa, dt, cd, D):
+    """Tens of thousands of tokens, weights spread over all of them: the mean error is the
+    output's rounding and little more.  (Two 16-bit parts of the weights 2^-22, for bf16
+    under an 8-bit cache too; sums in 32 bits.)"""
+    b = Batch(dt, cd, [30000, 9001], [1, 1], 4, 1, D, 16, 61)
+    got = _decode(pa, b).cpu().double()
+    want, _, _ = b.want()
+    for s in range(2):
+        rounded = want[s].to(b.dt).double()
+        assert _off(got[s], want[s]) <= 1.05 * _off(rounded, want[s]) + 5e-6
