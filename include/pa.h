@@ -340,7 +340,7 @@ PA_API size_t pa_decode_masked_workspace_bytes(int num_seqs, int num_heads, int 
  *   softcap, alibi_slopes, window   as pa_decode_masked.
  *   Other arguments as pa_prefill; num_heads / num_kv_heads <= 128, any number.  Also
  *   head_dim 64, fp32, and quantised caches (k_scale, v_scale as pa_decode_v1): these run
- *   on the CUDA cores, one warp per row and head (about 3 TFLOP/s), for completeness.
+ *   on the CUDA cores, one warp per row and head (1.3 to 2.4 TFLOP/s), for completeness.
  *   A row that sees nothing gets zeros.  Unseen rows of K and V do not reach a row's
  *   output, whatever they hold; blocks that end before the first token that any row of the
  *   sequence sees are not looked up.  A sequence whose lengths or query rows are out of range

@@ -13,9 +13,11 @@
 // the second launch of the persistent decode, and the choice of form.  The tensor-core
 // forms are the MASK builds of pa_decode_kernel.cuh and pa_fused_kernel.cuh and the MOD
 // builds of pa_prefill_kernel.cuh.  Decode is bound by the cache's bytes: 8 x 32k tokens,
-// bf16, with scores (1.04 GB) 201 us, 172 of them in the attention launch (6.0 TB/s);
-// 32 x 640, fp16, capped (85 MB) 18.4 us; 64 windows of 4096, FP8 (552 MB) 142 us, there
-// by the widening of the codes (ALU pipe 58% busy).
+// bf16, with scores (1.04 GB) 202 us, 172 of them in the attention launch (6.0 TB/s);
+// 32 x 640, fp16, capped (85 MB) 18.8 us; 64 windows of 4096, bf16 over FP8 (552 MB) 146 us,
+// there by the widening of the codes (ALU pipe 58% busy).  The CUDA-core form is bound by
+// its one chain of loads and exponentials per row and head: 1.3 to 2.4 TFLOP/s in prefill, and
+// 29 ms for 8 x 32k tokens in fp32, 5 times the plain fp32 decode.
 #include "pa_decode_kernel.cuh"
 #include "pa_fused_kernel.cuh"
 #include "pa_write.cuh"

@@ -1,7 +1,7 @@
 // pa_prefill_kernel.cuh -- the kernel of pa_prefill and pa_decode_cascade (pa_prefill.cu)
 // and, with changed scores, of pa_prefill_masked (pa_prefill_masked.cu): multi-token
-// query over the paged KV cache on the 5th-generation tensor cores (tcgen05): a chunk of new tokens per sequence
-// attends to its cached prefix and, causally, to itself.  This is the prefill
+// query over the paged KV cache on the 5th-generation tensor cores (tcgen05): a chunk of new
+// tokens per sequence attends to its cached prefix and, causally, to itself.  This is the prefill
 // that automatic prefix caching leaves to compute: the second request sharing
 // a cached prompt computes only its new tokens
 // ("LLM推理优化：vLLM PagedAttention深度解析与工程实践" §4.2;
@@ -10,7 +10,7 @@
 // A query tile packs TQ = 128 / G query tokens x the G query heads of one kv
 // head (row m = token m / G, head m % G), so every K/V byte loaded serves the
 // whole GQA group.  One CTA holds two such tiles (A and B) and plays four
-// roles with its 10 warps:
+// roles with its 10 warps (11 with MOD >= 0, below):
 //   warp 8      TMA: Q once, then 128-token K and V tiles (one box per block
 //               and 64-column half) into rings of 3 (K) and 2 (V) stages, K
 //               running one tile ahead of V;
@@ -31,8 +31,7 @@
 //               instruction issue, not by the 16 exponentials per clock of the
 //               special-function unit (moving a share of them to a polynomial
 //               on the FMA pipe made it slower).
-// 128-token tiles keep every MMA at N = 128: a tcgen05.mma of N = 64 costs
-// about as long as one of N = 128, so narrower tiles halve the tensor rate.
+// 128-token tiles (the MOD builds take them in 64-token steps) halve the hand-offs a token.
 // P over S needs one order the hardware does not give by itself: S_x(j+1)
 // may overwrite P_x(j) only once PV_x(j) has completed, so the MMA thread
 // waits for PV_x(j)'s commit before it issues S_x(j+1).
@@ -65,14 +64,15 @@
 //   tile's KV tiles; each leaves O and (m, l) in its shared memory, and the cluster merges
 //   them row by row through distributed shared memory (no workspace, a fixed order).
 // * P goes in as two parts for fp16 too: one part's rounding alone is as large as the
-//   output's.
+//   output's.  (bf16's two are 16 bits, 0.2% of the outputs round the other way than from P
+//   in 32 bits, with no larger error; fp16's are 22.)
 // * V rows that no row of the CTA sees are zeroed; a row that comes out non-finite (a
 //   V row that other rows see holds infinities or NaN: 0 * inf in the product) is computed
 //   again from its own tokens alone.
-// Bound: the softmax's instructions and the tensor core about evenly (issue 56%, tensor
-// pipe 49%, ALU 47%, FMA 40% busy on the capped bf16 case).  8 x (4096 cached + 512 new),
-// 64/8 heads, bf16, cap: 0.91 ms, 645 TFLOP/s; 2 x 4096 whole prompts, fp16, prefix and bias:
-// 0.87 to 0.94 ms (clocks under the power cap).
+// Bound: the softmax's instructions and the tensor core about evenly (issue 55%, tensor
+// pipe 47%, ALU 47%, FMA 39% busy on the capped bf16 case).  8 x (4096 cached + 512 new),
+// 64/8 heads, bf16, cap: 1.02 ms, 575 TFLOP/s (one launch alone, off the power cap, 0.96); 2 x
+// 4096 whole prompts, fp16, prefix and bias: 0.96 ms, 608 TFLOP/s (0.88).
 #pragma once
 
 #include <cooperative_groups.h>

@@ -42,7 +42,7 @@ template <typename ST, int MODE, int D>
 __global__ void __launch_bounds__(kThreads, sizeof(ST) == 2 && MODE == kWriteCopy ? 10 : 1)
     rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int VE = 16 / static_cast<int>(sizeof(ST));
-  constexpr int LPR = D / (2 * VE);            // lanes per row: 8 (16-bit, D 128) .. 16
+  constexpr int LPR = D / (2 * VE);            // lanes per row: 4 (16-bit, D 64) .. 16 (fp32, D 128)
   constexpr int RPP = kThreads / LPR;          // rows per pass
   struct alignas(16) Vec {
     ST v[VE];
